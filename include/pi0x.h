@@ -44,10 +44,13 @@ enum {
   PI0X_FP32 = 1   /* every operation in fp32 (no TF32) */
 };
 
-/* ---- element type of weight arrays handed to pi0x_create -------------------- */
+/* ---- element types: weight arrays handed to pi0x_create (bf16, f32), and the rows
+ * and pages of the paged cache below ------------------------------------------- */
 enum {
   PI0X_DTYPE_BF16 = 0,  /* uint16 bf16 bit patterns */
-  PI0X_DTYPE_F32 = 1
+  PI0X_DTYPE_F32 = 1,
+  PI0X_DTYPE_E4M3 = 2,  /* cache pages only: 8-bit floats with one fp32 scale a row */
+  PI0X_DTYPE_INT8 = 3   /* cache pages only: 8-bit integers with one fp32 scale a row */
 };
 
 /* Dimensions.  The library is compiled for width 1024, mlp_dim 4096, 8 query
@@ -130,6 +133,116 @@ int pi0x_sample(pi0x_handle *h, const void *const *prefix_k, const void *const *
  * Returns PI0X_OK, PI0X_ETIMEOUT (a bounded device wait gave up; the outputs
  * of that call are invalid), PI0X_EDEVICE or PI0X_ECUDA.  Clears the word. */
 int pi0x_sync_status(pi0x_handle *h);
+
+/* ---- paged prefix cache --------------------------------------------------------
+ * pi0x_sample takes the prefix keys and values as contiguous bf16 tensors.  The
+ * calls below make and hold them: per-head norm and rotation of queries and keys
+ * (pi0x_qk_norm_rope), a cache in pages shared by many samples, in bf16 or 8 bits
+ * (pi0x_cache_write, pi0x_cache_read), attention of one new token a sample over it
+ * (pi0x_cache_attention) and the denoising loop on it (pi0x_sample_cache).
+ *
+ * Every pointer below is device memory of the current device.  The calls enqueue
+ * their work on `stream` and return; they allocate nothing, keep nothing, and may be
+ * captured into a CUDA graph (pi0x_sample_cache excepted).  What can be seen from the host is checked
+ * (PI0X_EINVAL, PI0X_EUNSUPPORTED); what lies in device memory is bounded by the
+ * kernels: a page table entry outside [0, num_pages) is a page without keys (nothing
+ * is read or written there), a length below 0 counts as 0 and one above the table's
+ * max_pages * page_size as that. */
+
+/* Pages of `page_size` rows for each of `layers` layers.  A row is one position's
+ * (kv_heads, head_dim) keys or values; in the 8-bit types every (row, head) has an
+ * fp32 scale and stands for code * scale.  kv_heads >= 1; head_dim 64, 128 or 256;
+ * layers >= 1; layers * num_pages * page_size < 2^31. */
+typedef struct {
+  void *k, *v;               /* (layers, num_pages, page_size, kv_heads, head_dim), 16-byte aligned */
+  float *k_scale, *v_scale;  /* (layers, num_pages, page_size, kv_heads); NULL for bf16 pages */
+  int layers, num_pages, page_size, kv_heads, head_dim;
+  int dtype;                 /* PI0X_DTYPE_BF16, PI0X_DTYPE_E4M3 or PI0X_DTYPE_INT8 */
+} pi0x_cache;
+
+/* Rows of `head_dim` contiguous elements at data + b * batch_stride + t * token_stride
+ * + h * head_stride (elements); data and the strides are multiples of 16 bytes. */
+typedef struct {
+  void *data;
+  int64_t batch_stride, token_stride, head_stride;
+} pi0x_rows;
+
+/* What is done to queries and keys: y = x * rsqrt(mean(x^2) + eps) * (1 + gain) over
+ * each head's row where a gain is given, then the rotate-half rotation of the pairs
+ * (i, i + head_dim/2) by pos * rope_base^(-2i/head_dim) where rope_base > 0 (1 or
+ * more).  The angle is exact to 2^-32 of a turn at every 32-bit position; all of it
+ * is fp32, rounded once to the output's type. */
+typedef struct {
+  const float *q_gain, *k_gain;  /* (head_dim) fp32, 16-byte aligned; NULL: no norm */
+  const int32_t *positions;      /* (B, T); NULL: start[b] + t */
+  float eps;                     /* > 0 where a gain is given */
+  float rope_base;               /* 0: no rotation */
+} pi0x_rotation;
+
+/* Norm and rotate q (B, T, q_heads, head_dim) into q_out and k (B, T, k_heads,
+ * head_dim) into k_out, all of `dtype` (PI0X_DTYPE_BF16 or PI0X_DTYPE_F32).  Either
+ * may be left out (0 heads, NULL); an output may be its input's memory, row for row.
+ * start: (B) first position of each sample (NULL: 0), not used with rot->positions. */
+int pi0x_qk_norm_rope(int dtype, int B, int T, int q_heads, int k_heads, int head_dim, const pi0x_rows *q,
+                      const pi0x_rows *k, const int32_t *start, const pi0x_rotation *rot, const pi0x_rows *q_out,
+                      const pi0x_rows *k_out, void *stream);
+
+/* Write the keys and values of T new tokens a sample, k and v (B, T, kv_heads,
+ * head_dim) of `dtype` (bf16 or f32), into the pages of `layer`.  Token t of sample b
+ * goes to slot pos = start[b] + t: row pos % page_size of page
+ * page_table[b * max_pages + pos / page_size].  A token at t >= count[b] (count NULL:
+ * T), at a negative slot or past the table is left out, and so is one whose page is
+ * outside the pool; slots without a new token keep what they hold.  Samples that
+ * share a page must not write the same slot.
+ *   rot != NULL: keys are normed and rotated first, and so is q (B, T, q_heads,
+ * head_dim), if given, into q_out - every (b, t) of it, whatever count says.
+ *   8-bit pages: int8 codes are rn(x / scale) with scale = max|x| / 127 of the row,
+ * e4m3 codes with the least power of two that brings max|x| within 448 (neither below
+ * 2^-126).  A row with a NaN or an infinity gets a NaN scale: it stands for NaN. */
+int pi0x_cache_write(const pi0x_cache *cache, int layer, int dtype, int B, int T, const pi0x_rows *k,
+                     const pi0x_rows *v, const int32_t *page_table, int max_pages, const int32_t *start,
+                     const int32_t *count, const pi0x_rotation *rot, int q_heads, const pi0x_rows *q,
+                     const pi0x_rows *q_out, void *stream);
+
+/* Read slots 0..P-1 of every sample for layers [layer0, layer0 + layers) into
+ * contiguous k_out, v_out (layers, B, kv_heads, P, head_dim) of `dtype` (bf16 or
+ * f32): with one kv head, the layout pi0x_sample takes layer by layer.  Slot p holds
+ * a key if p < lens[b], its page is inside the pool and mask (B, P) uint8 (NULL: all)
+ * is nonzero there; the others are not read and come out as zeros.  mask_out (B, P)
+ * uint8 (may be NULL) gets 1 where there is a key, else 0. */
+int pi0x_cache_read(const pi0x_cache *cache, int layer0, int layers, int B, int P, const int32_t *page_table,
+                    int max_pages, const int32_t *lens, const uint8_t *mask, int dtype, void *k_out, void *v_out,
+                    uint8_t *mask_out, void *stream);
+
+/* Attention of one new token a sample over the pages of `layer`: q (B, q_heads,
+ * head_dim) bf16 (q->token_stride is not used), query head h reads kv head
+ * h / (q_heads / kv_heads); q_heads is a multiple of kv_heads.  Keys are the slots p <
+ * lens[b] whose page is inside the pool and, with mask (B, mask_len) uint8, p <
+ * mask_len and mask[b][p] nonzero; nothing else is read.
+ *   out (B, q_heads, head_dim) bf16 = softmax(scale * q . k) v; lse (B, q_heads) fp32
+ * (may be NULL) = log of the sum of exp(scale * q . k).  A sample without a key gets
+ * zeros and -inf.  Sums and softmax statistics are fp32; probabilities are rounded to
+ * the 16-bit type of the matrix product.  The result of a call does not depend on
+ * timing.
+ *   workspace: pi0x_cache_attention_workspace() bytes, 16-byte aligned, used by this
+ * call only while it runs: calls that may overlap need one each. */
+int pi0x_cache_attention(const pi0x_cache *cache, int layer, int B, int q_heads, const pi0x_rows *q,
+                         const int32_t *page_table, int max_pages, const int32_t *lens, const uint8_t *mask,
+                         int mask_len, float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/* Bytes of workspace a pi0x_cache_attention call of these sizes needs (0 if none, or
+ * if the sizes are refused). */
+size_t pi0x_cache_attention_workspace(const pi0x_cache *cache, int B, int q_heads, int max_pages);
+
+/* pi0x_sample with the prefix K/V of a cache: reads slots 0..P-1 of all layers, as
+ * pi0x_cache_read with `lens` and `mask` does, into buffers of the handle and runs the
+ * loop on them.  The cache has the handle's depth, one kv head and head_dim 256.
+ * state, x1, x0 as for pi0x_sample (device or host); page_table, lens and mask are
+ * device memory. */
+int pi0x_sample_cache(pi0x_handle *h, const pi0x_cache *cache, int B, int P, const int32_t *page_table,
+                      int max_pages, const int32_t *lens, const uint8_t *mask, const float *state, const float *x1,
+                      int num_steps, float *x0, void *stream);
 
 /* ---- solver / convention variants --------------------------------------------
  * The default is pi0's own loop (`sample_actions` / `denoise_step` on the

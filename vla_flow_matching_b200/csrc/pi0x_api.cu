@@ -13,6 +13,7 @@
 
 #include "../../include/pi0x.h"
 #include "../../include/pi0x_debug.h"
+#include "cache.cuh"
 #include "common.cuh"
 #include "kernels.cuh"
 
@@ -1151,6 +1152,46 @@ int pi0x_sample(pi0x_handle *h, const void *const *prefix_k, const void *const *
   h->last_stream = s;
   h->called = true;
   return PI0X_OK;
+}
+
+int pi0x_sample_cache(pi0x_handle *h, const pi0x_cache *cache, int B, int P, const int32_t *page_tab, int max_pages,
+                      const int32_t *lens, const uint8_t *mask, const float *state, const float *x1, int num_steps,
+                      float *x0, void *stream) {
+  if (!h || !lens || !state || !x1 || !x0 || B < 1 || B > 4096 || P < 1 || P > 8192 || num_steps < 1 ||
+      num_steps > 1024)
+    return PI0X_EINVAL;
+  int st = check_cache(cache, 0, h->cfg.depth, B, page_tab, max_pages);
+  if (st) return st;
+  if (cache->layers != h->cfg.depth || cache->kv_heads != 1 || cache->head_dim != kHeadDim) {
+    g_last_error = "pi0x_sample_cache: the cache must have the handle's depth, one kv head and head_dim 256";
+    return PI0X_EINVAL;
+  }
+  const int L = h->cfg.depth;
+  st = ensure_workspace(h, B, P, num_steps);  // before the buffers below: it may wait for the last call
+  if (!st) st = ensure_stage(h, B, P);
+  if (st) return st;
+  Workspace &ws = h->ws;
+  ReadArgs a = {};
+  a.layers = L;
+  a.B = B;
+  a.kv = 1;
+  a.P = P;
+  a.layer_rows = (int64_t)cache->num_pages * cache->page_size;
+  a.kp = layer_pool(cache, 0, false);
+  a.vp = layer_pool(cache, 0, true);
+  a.pt = page_table(cache, page_tab, max_pages);
+  a.lens = lens;
+  a.mask = mask;
+  a.k_out = ws.st_k;
+  a.v_out = ws.st_v;
+  a.mask_out = ws.st_mask;
+  CK(launch_cache_read(a, PI0X_DTYPE_BF16, cache->dtype, kHeadDim, (cudaStream_t)stream));
+  const void *pk[kMaxDepth], *pv[kMaxDepth];
+  for (int l = 0; l < L; ++l) {
+    pk[l] = ws.st_k + (size_t)l * B * P * kHeadDim;
+    pv[l] = ws.st_v + (size_t)l * B * P * kHeadDim;
+  }
+  return pi0x_sample(h, pk, pv, ws.st_mask, B, P, state, x1, num_steps, x0, stream);
 }
 
 int pi0x_sync_status(pi0x_handle *h) {

@@ -16,14 +16,15 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpi0x.so
 
 PI0X_OK, PI0X_EINVAL, PI0X_EUNSUPPORTED, PI0X_ENOMEM, PI0X_ECUDA, PI0X_ETIMEOUT, PI0X_EDEVICE = range(7)
 PI0X_BF16, PI0X_FP32 = 0, 1
-PI0X_DTYPE_BF16, PI0X_DTYPE_F32 = 0, 1
+PI0X_DTYPE_BF16, PI0X_DTYPE_F32, PI0X_DTYPE_E4M3, PI0X_DTYPE_INT8 = range(4)
 
 #: Every symbol include/pi0x.h declares.
 EXPORTED = ["pi0x_create", "pi0x_sample", "pi0x_sync_status", "pi0x_launch_count",
             "pi0x_status_string", "pi0x_last_error", "pi0x_destroy", "pi0x_version",
             "pi0x_debug_gemm_bf16", "pi0x_debug_attention", "pi0x_profile_enable", "pi0x_profile_read",
             "pi0x_set_variant", "pi0x_attention_noalloc", "pi0x_uses_loop", "pi0x_debug_loop_stall",
-            "pi0x_debug_set_loop"]
+            "pi0x_debug_set_loop", "pi0x_qk_norm_rope", "pi0x_cache_write", "pi0x_cache_read",
+            "pi0x_cache_attention", "pi0x_cache_attention_workspace", "pi0x_sample_cache"]
 
 #: time grids of pi0x_set_variant
 PI0X_TIME_PI0 = 0
@@ -63,6 +64,22 @@ _TOP_FIELDS = ("state_proj_w", "state_proj_b", "action_in_w", "action_in_b", "ti
 class Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in _TOP_FIELDS] + [
         ("layers", ctypes.POINTER(LayerWeights)), ("dtype", ctypes.c_int)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)] + [
+        (n, ctypes.c_int) for n in ("layers", "num_pages", "page_size", "kv_heads", "head_dim", "dtype")]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Rotation(ctypes.Structure):
+    _fields_ = [("q_gain", ctypes.c_void_p), ("k_gain", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("rope_base", ctypes.c_float)]
 
 
 _lib = None
@@ -117,6 +134,21 @@ def load() -> ctypes.CDLL:
     lib.pi0x_profile_read.argtypes = [ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(ctypes.c_long),
                                       ctypes.POINTER(ctypes.c_double)]
     lib.pi0x_profile_read.restype = ctypes.c_int
+    ptr, cint, rows, cache = ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(Rows), ctypes.POINTER(Cache)
+    lib.pi0x_qk_norm_rope.argtypes = [cint] * 6 + [rows, rows, ptr, ctypes.POINTER(Rotation), rows, rows, ptr]
+    lib.pi0x_qk_norm_rope.restype = cint
+    lib.pi0x_cache_write.argtypes = [cache, cint, cint, cint, cint, rows, rows, ptr, cint, ptr, ptr,
+                                     ctypes.POINTER(Rotation), cint, rows, rows, ptr]
+    lib.pi0x_cache_write.restype = cint
+    lib.pi0x_cache_read.argtypes = [cache, cint, cint, cint, cint, ptr, cint, ptr, ptr, cint, ptr, ptr, ptr, ptr]
+    lib.pi0x_cache_read.restype = cint
+    lib.pi0x_cache_attention.argtypes = [cache, cint, cint, cint, rows, ptr, cint, ptr, ptr, cint, ctypes.c_float,
+                                         ptr, ptr, ptr, ctypes.c_size_t, ptr]
+    lib.pi0x_cache_attention.restype = cint
+    lib.pi0x_cache_attention_workspace.argtypes = [cache, cint, cint, cint]
+    lib.pi0x_cache_attention_workspace.restype = ctypes.c_size_t
+    lib.pi0x_sample_cache.argtypes = [ptr, cache, cint, cint, ptr, cint, ptr, ptr, ptr, ptr, cint, ptr, ptr]
+    lib.pi0x_sample_cache.restype = cint
     _lib = lib
     return lib
 
@@ -165,6 +197,295 @@ def attention_noalloc(q, ks, vs, prefix_k, prefix_v, mask, B, H, P, step0, out, 
                                          B, H, P, int(step0), _ptr(out), ctypes.c_void_p(stream)),
            "pi0x_attention_noalloc")
     return out
+
+
+def _device_of(what: str, *tensors):
+    """The CUDA device that every given tensor (None: left out) lies on."""
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{what}: every tensor must be on a CUDA device")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError(f"{what}: tensors on {device} and {t.device}")
+    return device
+
+
+class _on:
+    """Makes `device` current for the calls inside, and gives its current stream."""
+
+    def __init__(self, device):
+        import torch
+        self._guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
+        self._stream = torch.cuda.current_stream
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return self._stream().cuda_stream
+
+    def __exit__(self, *e):
+        if self._guard is not None:
+            self._guard.__exit__(*e)
+
+
+def _row_type(what: str, t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return PI0X_DTYPE_BF16
+    if t.dtype == torch.float32:
+        return PI0X_DTYPE_F32
+    raise ValueError(f"{what}: rows are bfloat16 or float32, not {t.dtype}")
+
+
+def _rows(what: str, t, B: int, T: int, dtype=None, head_dim=None) -> Rows:
+    """(B, T, heads, head_dim) tensor as strided rows."""
+    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != T or t.stride(3) != 1 or \
+            (head_dim is not None and t.shape[3] != head_dim) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what}: expected ({B}, {T}, heads, {head_dim or 'head_dim'}) rows of one type with a "
+                         f"contiguous last dimension, got {tuple(t.shape)} {t.dtype}")
+    s = t.stride()
+    return Rows(t.data_ptr(), s[0], s[1], s[2])
+
+
+def _ints(what: str, name: str, t, *shape):
+    import torch
+    if t is None:
+        return 0
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: {name} must be a contiguous int32 tensor of shape {shape}")
+    return t.data_ptr()
+
+
+def _bytes(what: str, name: str, t, B: int):
+    import torch
+    if t is None:
+        return 0, 0
+    if t.dtype not in (torch.uint8, torch.bool) or t.dim() != 2 or t.shape[0] != B or t.shape[1] < 1 or \
+            not t.is_contiguous():
+        raise ValueError(f"{what}: {name} must be a contiguous uint8 or bool tensor of shape ({B}, 1 or more)")
+    return t.data_ptr(), t.shape[1]
+
+
+def _gain(what: str, t, head_dim: int):
+    import torch
+    if t is None:
+        return 0
+    if t.dtype != torch.float32 or tuple(t.shape) != (head_dim,) or not t.is_contiguous():
+        raise ValueError(f"{what}: a gain is a contiguous float32 tensor of shape ({head_dim},)")
+    return t.data_ptr()
+
+
+def _out(what: str, t, like):
+    """`t`, or a new tensor like `like` (its shape, contiguous)."""
+    import torch
+    if t is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if t.dtype != like.dtype or t.shape != like.shape:
+        raise ValueError(f"{what}: an output must have its input's shape and type")
+    return t
+
+
+def qk_norm_rope(q, k=None, start=None, *, positions=None, q_gain=None, k_gain=None, eps: float = 1e-6,
+                 rope_base: float = 10000.0, q_out=None, k_out=None):
+    """Per-head RMSNorm (where a gain is given: gain 1 + g) and rotate-half rotation of
+    queries and keys in one pass (pi0x_qk_norm_rope).
+
+    ``q`` (B, T, heads, D) and ``k`` (B, T, kv_heads, D) or None: bf16 or fp32 CUDA
+    tensors, D 64, 128 or 256, any strides in whole 16 bytes with a contiguous last
+    dimension.  Token t of sample b has position ``positions[b, t]``, or
+    ``start[b] + t`` (start None: 0).  ``rope_base`` None: no rotation.  Returns
+    (q_out, k_out), new tensors unless given; an output may be its own input.
+    Runs on the current stream of the tensors' device.
+    """
+    what = "qk_norm_rope"
+    device = _device_of(what, q, k, start, positions, q_gain, k_gain, q_out, k_out)
+    dtype = _row_type(what, q)
+    B, T, heads, D = q.shape if q.dim() == 4 else (0, 0, 0, 0)
+    rq = _rows(what, q, B, T)
+    rk = _rows(what, k, B, T, q.dtype, D) if k is not None else None
+    with _on(device) as stream:
+        q_out = _out(what, q_out, q)
+        k_out = _out(what, k_out, k) if k is not None else None
+        rot = Rotation(_gain(what, q_gain, D), _gain(what, k_gain, D),
+                       _ints(what, "positions", positions, B, T), eps, rope_base or 0.0)
+        if q.numel() == 0:
+            return q_out, k_out
+        _check(load().pi0x_qk_norm_rope(
+            dtype, B, T, heads, k.shape[2] if k is not None else 0, D, rq, rk, _ints(what, "start", start, B), rot,
+            _rows(what, q_out, B, T), _rows(what, k_out, B, T) if k is not None else None, stream),
+            "pi0x_qk_norm_rope")
+    return q_out, k_out
+
+
+class KVCache:
+    """A paged key-value cache (pi0x_cache) over torch tensors.
+
+    ``k``, ``v``: (layers, num_pages, page_size, kv_heads, head_dim) contiguous pools of
+    bfloat16, float8_e4m3fn or int8; ``k_scale``, ``v_scale``: (layers, num_pages,
+    page_size, kv_heads) float32, for the 8-bit types.  :meth:`empty` makes them.
+    Which pages a sample has is the caller's: every method takes ``table`` (B,
+    max_pages) int32 page numbers; an entry outside the pool holds no keys.  Methods
+    run on the current stream of the cache's device, and may be captured into a graph.
+    """
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        types = {torch.bfloat16: PI0X_DTYPE_BF16, torch.float8_e4m3fn: PI0X_DTYPE_E4M3, torch.int8: PI0X_DTYPE_INT8}
+        if k.dtype not in types or k.dtype != v.dtype or k.dim() != 5 or k.shape != v.shape or \
+                not k.is_contiguous() or not v.is_contiguous():
+            raise ValueError("KVCache: k and v must be contiguous (layers, num_pages, page_size, kv_heads, head_dim) "
+                             "tensors of one type: bfloat16, float8_e4m3fn or int8")
+        scaled = k.dtype != torch.bfloat16
+        if scaled != (k_scale is not None) or scaled != (v_scale is not None):
+            raise ValueError("KVCache: 8-bit pools need k_scale and v_scale, bfloat16 pools take none")
+        for s in (k_scale, v_scale):
+            if s is not None and (s.dtype != torch.float32 or s.shape != k.shape[:4] or not s.is_contiguous()):
+                raise ValueError("KVCache: scales must be contiguous float32 (layers, num_pages, page_size, kv_heads)")
+        self.device = _device_of("KVCache", k, v, k_scale, v_scale)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.layers, self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
+        self._desc = Cache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), *k.shape, types[k.dtype])
+        self._lib = load()
+
+    @classmethod
+    def empty(cls, layers: int, num_pages: int, page_size: int, kv_heads: int = 1, head_dim: int = 256,
+              dtype: str = "bf16", device="cuda"):
+        """A cache of zeros; ``dtype`` "bf16", "e4m3" or "int8"."""
+        import torch
+        types = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+        if dtype not in types:
+            raise ValueError(f"KVCache: dtype is one of {sorted(types)}")
+        shape = (layers, num_pages, page_size, kv_heads, head_dim)
+        pools = [torch.zeros(shape, dtype=types[dtype], device=device) for _ in range(2)]
+        if dtype != "bf16":
+            pools += [torch.zeros(shape[:4], dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*pools)
+
+    def _on(self, what: str, *tensors):
+        device = _device_of(what, *tensors)
+        if device != self.device:
+            raise ValueError(f"{what}: tensors on {device}, the cache on {self.device}")
+        return _on(device)
+
+    def _table(self, what: str, table):
+        if table.dim() != 2:
+            raise ValueError(f"{what}: table must be a contiguous int32 tensor (batch, max_pages)")
+        return _ints(what, "table", table, *table.shape)
+
+    def write(self, layer: int, k, v, table, start, count=None, *, q=None, q_out=None, positions=None, q_gain=None,
+              k_gain=None, eps: float = 1e-6, rope_base: Optional[float] = None):
+        """Write T new tokens a sample into the pages of ``layer`` (pi0x_cache_write).
+
+        ``k``, ``v`` (B, T, kv_heads, head_dim) bf16 or fp32; token t of sample b goes to
+        slot ``start[b] + t``; those at t >= ``count[b]`` (None: T) are left out.  With
+        ``rope_base`` or a gain, keys are normed and rotated first as by
+        :func:`qk_norm_rope`, and so is ``q`` (B, T, heads, head_dim), in the same pass.
+        Returns ``q_out`` (new unless given), or None without q.
+        """
+        what = "KVCache.write"
+        on = self._on(what, k, v, table, start, count, q, q_out, positions, q_gain, k_gain)
+        dtype = _row_type(what, k)
+        B, T = k.shape[:2]
+        D = self.head_dim
+        rk, rv = _rows(what, k, B, T, head_dim=D), _rows(what, v, B, T, k.dtype, D)
+        if k.shape[2] != self.kv_heads or v.shape[2] != self.kv_heads:
+            raise ValueError(f"{what}: k and v have {k.shape[2]} and {v.shape[2]} heads, the cache {self.kv_heads}")
+        if table.shape[0] != B:
+            raise ValueError(f"{what}: table has {table.shape[0]} samples, k has {B}")
+        rot = None
+        if q is not None or rope_base or q_gain is not None or k_gain is not None:
+            rot = Rotation(_gain(what, q_gain, D), _gain(what, k_gain, D),
+                           _ints(what, "positions", positions, B, T), eps, rope_base or 0.0)
+        rq = _rows(what, q, B, T, k.dtype, D) if q is not None else None
+        if start is None:
+            raise ValueError(f"{what}: start is required")
+        with on as stream:
+            if q is not None:
+                q_out = _out(what, q_out, q)
+            if k.numel() == 0:
+                return q_out
+            _check(self._lib.pi0x_cache_write(
+                self._desc, layer, dtype, B, T, rk, rv, self._table(what, table), table.shape[1],
+                _ints(what, "start", start, B), _ints(what, "count", count, B), rot,
+                q.shape[2] if q is not None else 0, rq, _rows(what, q_out, B, T) if q is not None else None, stream),
+                "pi0x_cache_write")
+        return q_out
+
+    def read(self, table, lens, length: int, *, mask=None, layer0: int = 0, layers: Optional[int] = None, dtype=None,
+             k_out=None, v_out=None, mask_out=None):
+        """Slots 0..length-1 of ``layers`` layers from ``layer0`` (None: to the last) as
+        contiguous (layers, B, kv_heads, length, head_dim) keys and values of ``dtype``
+        (bfloat16, the default, or float32), and a (B, length) uint8 mask of the slots
+        that hold a key: below ``lens[b]``, on a page of the pool and, with ``mask`` (B,
+        length), nonzero there.  The others come out as zeros (pi0x_cache_read).
+        """
+        import torch
+        what = "KVCache.read"
+        on = self._on(what, table, lens, mask, k_out, v_out, mask_out)
+        B = table.shape[0]
+        n = self.layers - layer0 if layers is None else layers
+        dtype = dtype or torch.bfloat16
+        m, mask_len = _bytes(what, "mask", mask, B)
+        if mask is not None and mask_len != length:
+            raise ValueError(f"{what}: mask covers {mask_len} slots, not {length}")
+        shape = (n, B, self.kv_heads, length, self.head_dim)
+        with on as stream:
+            outs = []
+            for t, sh, dt in ((k_out, shape, dtype), (v_out, shape, dtype), (mask_out, (B, length), torch.uint8)):
+                if t is None:
+                    t = torch.empty(sh, dtype=dt, device=self.device)
+                elif tuple(t.shape) != sh or t.dtype != dt or not t.is_contiguous():
+                    raise ValueError(f"{what}: outputs must be contiguous {shape} {dtype} and ({B}, {length}) uint8")
+                outs.append(t)
+            k_out, v_out, mask_out = outs
+            if k_out.numel() == 0 and n >= 1:
+                return k_out, v_out, mask_out
+            _check(self._lib.pi0x_cache_read(
+                self._desc, layer0, n, B, length, self._table(what, table), table.shape[1],
+                _ints(what, "lens", lens, B), m, _row_type(what, k_out), k_out.data_ptr(), v_out.data_ptr(),
+                mask_out.data_ptr(), stream), "pi0x_cache_read")
+        return k_out, v_out, mask_out
+
+    def attend(self, layer: int, q, table, lens, *, mask=None, scale: Optional[float] = None, out=None, lse=None):
+        """Attention of one new token a sample over the pages of ``layer``
+        (pi0x_cache_attention): ``q`` (B, heads, head_dim) bf16, heads a multiple of
+        kv_heads; keys are the slots below ``lens[b]`` on pages of the pool and, with
+        ``mask`` (B, length), below its length and nonzero there.  ``scale`` None:
+        head_dim ** -0.5.  Returns (out, lse): (B, heads, head_dim) bf16 and (B, heads)
+        fp32, zeros and -inf for a sample without keys.
+        """
+        import torch
+        what = "KVCache.attend"
+        on = self._on(what, q, table, lens, mask, out, lse)
+        if q.dim() != 3 or q.dtype != torch.bfloat16 or q.shape[2] != self.head_dim or q.stride(2) != 1:
+            raise ValueError(f"{what}: q must be (batch, heads, {self.head_dim}) bfloat16 with a contiguous last "
+                             "dimension")
+        B, heads, D = q.shape
+        if table.shape[0] != B:
+            raise ValueError(f"{what}: table has {table.shape[0]} samples, q has {B}")
+        m, mask_len = _bytes(what, "mask", mask, B)
+        with on as stream:
+            if out is None:
+                out = torch.empty((B, heads, D), dtype=torch.bfloat16, device=self.device)
+            if lse is None:
+                lse = torch.empty((B, heads), dtype=torch.float32, device=self.device)
+            if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or \
+                    lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous():
+                raise ValueError(f"{what}: out must be contiguous like q, lse contiguous float32 ({B}, {heads})")
+            if q.numel() == 0:
+                return out, lse
+            need = self._lib.pi0x_cache_attention_workspace(self._desc, B, heads, table.shape[1])
+            work = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+            s = q.stride()
+            _check(self._lib.pi0x_cache_attention(
+                self._desc, layer, B, heads, Rows(q.data_ptr(), s[0], 0, s[1]), self._table(what, table),
+                table.shape[1], _ints(what, "lens", lens, B), m, mask_len, D ** -0.5 if scale is None else scale,
+                out.data_ptr(), lse.data_ptr(), _ptr(work), need, stream), "pi0x_cache_attention")
+        return out, lse
 
 
 class Sampler:
@@ -238,6 +559,25 @@ class Sampler:
         _check(self._lib.pi0x_sample(self._h, pk, pv, _ptr(mask), B, P, _ptr(state), _ptr(x1),
                                      int(num_steps), _ptr(x0), ctypes.c_void_p(stream)),
                "pi0x_sample")
+        return x0
+
+    def sample_cache(self, cache: KVCache, table, lens, length: int, state, x1, num_steps: int, mask=None, x0=None):
+        """Enqueue one call whose prefix K/V are slots 0..length-1 of a paged cache, as
+        :meth:`KVCache.read` reads them (pi0x_sample_cache).  Runs on the current stream
+        of the cache's device."""
+        what = "Sampler.sample_cache"
+        on = cache._on(what, table, lens, mask)
+        if x0 is None:
+            x0 = x1.new_empty(x1.shape) if hasattr(x1, "new_empty") else np.empty_like(x1)
+        B = int(table.shape[0])
+        m, mask_len = _bytes(what, "mask", mask, B)
+        if mask is not None and mask_len != length:
+            raise ValueError(f"{what}: mask covers {mask_len} slots, not {length}")
+        with on as stream:
+            _check(self._lib.pi0x_sample_cache(
+                self._h, cache._desc, B, length, cache._table(what, table), int(table.shape[1]),
+                _ints(what, "lens", lens, B), m, _ptr(state), _ptr(x1), int(num_steps), _ptr(x0), stream),
+                "pi0x_sample_cache")
         return x0
 
     def set_variant(self, time_grid: int = PI0X_TIME_PI0, x_prediction: bool = False,
