@@ -152,7 +152,8 @@ int pi0x_sync_status(pi0x_handle *h);
 /* Pages of `page_size` rows for each of `layers` layers.  A row is one position's
  * (kv_heads, head_dim) keys or values; in the 8-bit types every (row, head) has an
  * fp32 scale and stands for code * scale.  kv_heads >= 1; head_dim 64, 128 or 256;
- * layers >= 1; layers * num_pages * page_size < 2^31. */
+ * layers >= 1; layers * num_pages * page_size < 2^31; a page table has fewer than 2^31 -
+ * 4096 slots. */
 typedef struct {
   void *k, *v;               /* (layers, num_pages, page_size, kv_heads, head_dim), 16-byte aligned */
   float *k_scale, *v_scale;  /* (layers, num_pages, page_size, kv_heads); NULL for bf16 pages */

@@ -33,9 +33,9 @@ struct PageTable {
 // Row of the pool that holds slot `pos` of sample b, or -1 (no page there).
 __host__ __device__ __forceinline__ int cache_row(const PageTable &pt, int b, int64_t pos) {
   if (pos < 0 || pos >= (int64_t)pt.max_pages * pt.page_size) return -1;
-  const int at = (int)(pos / pt.page_size), off = (int)(pos - (int64_t)at * pt.page_size);
+  const uint32_t at = (uint32_t)pos / (uint32_t)pt.page_size, off = (uint32_t)pos - at * (uint32_t)pt.page_size;
   const int page = pt.table[(int64_t)b * pt.max_pages + at];
-  return page >= 0 && page < pt.num_pages ? page * pt.page_size + off : -1;
+  return page >= 0 && page < pt.num_pages ? page * pt.page_size + (int)off : -1;
 }
 
 // ---- norm, rotation and page writes (k_cache.cu) ---------------------------------

@@ -82,8 +82,8 @@ int check_cache(const pi0x_cache *c, int layer0, int layers, int B, const int32_
   const int64_t most = INT32_MAX;
   if ((int64_t)c->num_pages * c->page_size > most / c->layers || c->kv_heads > 65535)
     return refuse(PI0X_EINVAL, "paged cache: 2^31 rows or more, or over 65535 kv heads");
-  if ((int64_t)max_pages * c->page_size > most)
-    return refuse(PI0X_EINVAL, "paged cache: a page table of 2^31 slots or more");
+  if ((int64_t)max_pages * c->page_size > most - 4096)  // kernels look a few blocks of keys ahead in 32 bits
+    return refuse(PI0X_EINVAL, "paged cache: a page table of 2^31 - 4096 slots or more");
   return PI0X_OK;
 }
 

@@ -2,94 +2,623 @@
 //
 // s_j = scale * q . k_j, out = sum_j e^(s_j - m) v_j / l, l = sum_j e^(s_j - m), with the
 // running maximum m and sum l of one pass over the keys.
+//
+// What bounds it: every key and value is read once and used by the query heads of its
+// kv head, at most 4 * heads / bytes-per-code operations a byte (16 for 8 heads in bf16),
+// far below the tensor cores' share, above what the FP32 pipes could do beside the loads.
+// So the products go to the tensor cores with the small side, the heads, as the 8
+// columns of m16n8k16: S^T = K Q^T takes 16 keys as rows, O^T = V^T P^T 16 dims.  With
+// these shapes both operands come straight from global memory into the registers that
+// the products read, with no shared memory between: a contraction may take its index in
+// any order, so a lane's 16 consecutive bytes of a key stand for whichever columns the
+// lane owns (q is read in the same order), and a product's rows may be any dims.
+//
+// A warp holds a step of 16 or more keys in registers (up to 8 KB of K and 8 KB of V),
+// loads the next keys while it works, and needs no barrier until its keys end.
 #include "cache.cuh"
 #include "common.cuh"
 #include "kernels.cuh"
 
-#include <cuda_fp8.h>
 #include <math.h>
 
 namespace pi0x {
 
 namespace {
 constexpr int kWarps = 4;
+constexpr int kHeadsPerUnit = 8;  // query heads of one kv head that share a pass: the product's columns
+constexpr unsigned kFull = 0xffffffffu;
 
-__device__ __forceinline__ float code_value(const bf16 *p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float code_value(const __nv_fp8_e4m3 *p) { return (float)*p; }
-__device__ __forceinline__ float code_value(const int8_t *p) { return (float)*p; }
+// 16 or 8 bytes of a row into registers, zeros where there is no row.  Read once: not kept in L1.
+template <int N>
+__device__ __forceinline__ void load_codes(uint32_t (&r)[N], const void *p, bool valid) {
+  if constexpr (N == 4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3])
+        : "l"(p), "r"((int)valid)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+        "@p ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];\n\t}"
+        : "=&r"(r[0]), "=&r"(r[1])
+        : "l"(p), "r"((int)valid)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+// The 8x8 matrix of 16-bit elements spread over the warp, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ float log2_approx(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Code types.  halves(): two consecutive codes of a 32-bit word of codes as the 16-bit pair
+// of the product; 8-bit codes become fp16, which holds both types' values exactly.
+struct CodeBf16 {
+  static constexpr int kBytes = 2;
+  static constexpr bool kScaled = false;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&x);
+  }
+  static __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+};
+struct Code8 {
+  static constexpr int kBytes = 1;
+  static constexpr bool kScaled = true;
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __half2 x = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&x);
+  }
+  static __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+};
+struct CodeE4m3 : Code8 {
+  static __device__ __forceinline__ void halves(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+};
+struct CodeInt8 : Code8 {
+  // x + 128 as the low bits of an fp16 in [1024, 2048), whose steps are 1; minus 1152.
+  static __device__ __forceinline__ void halves(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const __half2 bias = __half2(__half_raw{0x6480}, __half_raw{0x6480});  // 1152
+    const uint32_t u = w ^ 0x80808080u;
+    uint32_t a = prmt(u, 0x64646464u, 0x4140), b = prmt(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&a), bias), y = __hsub2(*reinterpret_cast<__half2 *>(&b), bias);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+  }
+};
+
+// Shapes of a (code type, head_dim) variant.
+template <typename C, int D>
+struct Shape {
+  static constexpr int kRowBytes = D * C::kBytes;
+  static constexpr int kKChunks = kRowBytes / 64;                       // 16-byte pieces of a key a lane holds
+  static constexpr int kVBytes = kRowBytes >= 128 ? 16 : 8;             // bytes of a value a lane loads at once
+  static constexpr int kVChunks = kRowBytes / (8 * kVBytes);
+  static constexpr int kVElems = kVBytes / C::kBytes;
+  // keys a warp takes at once: 16 per product, more where rows are short, so that up to 4 KB
+  // of keys are on their way (8 KB at 512 bytes a row)
+  static constexpr int kTiles = kRowBytes >= 256 ? 1 : 256 / kRowBytes;
+  static constexpr int kKeys = 16 * kTiles;
+  static constexpr int kBlock = kWarps * kKeys;                         // keys of a scheduling block
+  static constexpr int kMTiles = D / 16;
+  static constexpr int kQPad = C::kBytes == 2 ? 64 : 16;                // bytes: keeps 8 heads' reads apart in the banks
+  static constexpr int kBlocksPerSm = kRowBytes >= 512 ? 2 : 3;
+};
+
+// Work: units u = (sample, kv head, group of up to 8 query heads), each of ceil(len/kBlock)
+// blocks of keys (at least one), laid end to end and shared out evenly over the grid: a CTA
+// takes `share` consecutive blocks, whichever units they belong to.  A unit inside one CTA is
+// finished there; of a longer one every CTA leaves its part (m, l and the unnormalised sum) in
+// the workspace, and k_attend_join adds them up in order.
+struct Part {
+  int unit;    // unit this CTA is the first of several CTAs of, or -1
+  int last;    // its last CTA
+  int slot;    // part of the first CTA; CTA c > first: part 2c
+};
+
+__device__ __forceinline__ int keys_of(const AttendArgs &a, int b) {
+  int64_t n = a.lens[b];
+  n = min(n, (int64_t)a.pt.max_pages * a.pt.page_size);
+  if (a.mask) n = min(n, (int64_t)a.mask_len);
+  return n > 0 ? (int)n : 0;
+}
+__host__ __device__ inline int head_groups(int heads, int kv) { return (heads / kv + kHeadsPerUnit - 1) / kHeadsPerUnit; }
+// Floats of a part: 8 heads' sums, then their m and l.
+template <int D>
+constexpr int kPartFloats = kHeadsPerUnit * D + 2 * kHeadsPerUnit;
+
 }  // namespace
 
-// One block a (sample, query head): warps take every fourth key, a lane D/32 dims.
 template <typename C, int D>
-__global__ void __launch_bounds__(kWarps * 32) k_attend(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_attend(const __grid_constant__ AttendArgs a) {
+  using S = Shape<C, D>;
   pdl_wait();
   pdl_trigger();
-  constexpr int E = D / 32;
-  __shared__ float sm_m[kWarps], sm_l[kWarps], sm_o[kWarps][D];
-  const int h = blockIdx.x, b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = h / (a.heads / a.kv);
-  float q[E], o[E], m = -INFINITY, l = 0.0f;
+  __shared__ __align__(16) float sm_o[kWarps][kHeadsPerUnit][D];
+  __shared__ __align__(16) uint8_t sm_q[kHeadsPerUnit][D * 2 + S::kQPad];
+  __shared__ float sm_m[kWarps][kHeadsPerUnit], sm_l[kWarps][kHeadsPerUnit], sm_qf[kHeadsPerUnit];
+  __shared__ int sm_scan[kWarps], sm_b, sm_at;
+  __shared__ int sm_total;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int group = a.heads / a.kv, groups = head_groups(a.heads, a.kv), upb = a.kv * groups;
+
+  // ---- this CTA's blocks [c0, c1) of all blocks, and the sample the first lies in
+  auto blocks_of = [&](int b) { return max(1, (keys_of(a, b) + S::kBlock - 1) / S::kBlock); };
+  const int per = (a.B + kWarps * 32 - 1) / (kWarps * 32), b_lo = min(a.B, tid * per), b_hi = min(a.B, b_lo + per);
+  int mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += blocks_of(b);
+  int incl = mine;
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    q[i] = __bfloat162float(a.q[b * a.q_sb + h * a.q_sh + lane + 32 * i]) * a.scale_log2;
-    o[i] = 0.0f;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
   }
-  const int64_t cap = (int64_t)a.pt.max_pages * a.pt.page_size;
-  int n = (int)min((int64_t)a.lens[b], cap);
-  if (a.mask) n = min(n, a.mask_len);
-  for (int p = warp; p < n; p += kWarps) {
-    if (a.mask && !a.mask[(int64_t)b * a.mask_len + p]) continue;
-    const int cell = cache_row(a.pt, b, p);
-    if (cell < 0) continue;
-    const int64_t at = (int64_t)cell * a.kv + g;
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) s += q[i] * code_value((const C *)a.kp.codes + at * D + lane + 32 * i);
-    s = warp_sum(s);
-    if (a.kp.scale) s *= a.kp.scale[at];
-    const float m2 = fmaxf(m, s), keep = m == -INFINITY ? 0.0f : exp2f(m - m2);
-    const float e = exp2f(s - m2), w = a.vp.scale ? e * a.vp.scale[at] : e;
-    l = l * keep + e;
-    m = m2;
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = o[i] * keep + w * code_value((const C *)a.vp.codes + at * D + lane + 32 * i);
-  }
-#pragma unroll
-  for (int i = 0; i < E; ++i) sm_o[warp][lane + 32 * i] = o[i];
-  if (lane == 0) sm_m[warp] = m, sm_l[warp] = l;
+  if (lane == 31) sm_scan[warp] = incl;
   __syncthreads();
-  float mm = -INFINITY, ll = 0.0f;
-  for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w]);
-  float f[kWarps];
+  int before = 0, total_b = 0;
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    f[w] = sm_m[w] == -INFINITY ? 0.0f : exp2f(sm_m[w] - mm);
-    ll += f[w] * sm_l[w];
+    if (w < warp) before += sm_scan[w];
+    total_b += sm_scan[w];
   }
-  for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-    float x = 0.0f;
-    for (int w = 0; w < kWarps; ++w) x += f[w] * sm_o[w][d];
-    a.out[((int64_t)b * a.heads + h) * D + d] = __float2bfloat16_rn(ll == 0.0f ? 0.0f : x / ll);
+  const int64_t total = (int64_t)total_b * upb;
+  const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t c0 = min(total, blockIdx.x * share), c1 = min(total, c0 + share);
+  Part *info = reinterpret_cast<Part *>(a.part) + blockIdx.x;
+  float *parts = a.part + (gridDim.x * sizeof(Part) / 4 + 3) / 4 * 4;
+  if (tid == 0) info->unit = -1;
+  {
+    int64_t off = (int64_t)(before + incl - mine) * upb;
+    if (c0 < c1 && c0 >= off && c0 < off + (int64_t)mine * upb) {
+      int b = b_lo;
+      for (;; ++b) {
+        const int64_t n = (int64_t)blocks_of(b) * upb;
+        if (c0 < off + n) break;
+        off += n;
+      }
+      sm_b = b;
+      sm_at = (int)(c0 - off);  // blocks into the sample's units
+    }
   }
-  if (threadIdx.x == 0 && a.lse) a.lse[(int64_t)b * a.heads + h] = ll == 0.0f ? -INFINITY : mm * 0.69314718f + logf(ll);
+  __syncthreads();
+  if (c0 >= c1) return;
+  int b = sm_b;
+  int64_t at = sm_at;
+
+  // ---- one segment after another: the blocks of one unit that are this CTA's
+  for (int64_t c = c0; c < c1;) {
+    const int len = keys_of(a, b), nblk = blocks_of(b);
+    const int ub = (int)(at / nblk), blk0 = (int)(at - (int64_t)ub * nblk);
+    const int nseg = (int)min((int64_t)(nblk - blk0), c1 - c);
+    const int h = ub / groups, h0 = h * group + (ub % groups) * kHeadsPerUnit;
+    const int nh = min(kHeadsPerUnit, group - (ub % groups) * kHeadsPerUnit);
+
+    // q: 16 threads a head.  fp16 products take q times a power of two (so that the largest
+    // element is in [1, 2)): exact for all that matters of a bf16 q.
+    {
+      constexpr int E = D / 16;
+      const int n = tid >> 4, e0 = (tid & 15) * E;
+      uint32_t w[E / 2];
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) w[i] = 0;
+      if (n < nh) {
+        const bf16 *src = a.q + b * a.q_sb + (h0 + n) * a.q_sh + e0;
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+          const uint2 v = *reinterpret_cast<const uint2 *>(src + 4 * i);
+          w[2 * i] = v.x, w[2 * i + 1] = v.y;
+        }
+      }
+      float factor = a.scale_log2;
+      if constexpr (C::kScaled) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+        const int e = min(max((int)(top >> 7), 1), 253);  // biased exponent of the largest element
+        const float down = __uint_as_float((uint32_t)(254 - e) << 23);
+        factor *= __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i)
+          w[i] = C::pack(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xffff0000u) * down);
+      }
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i)
+        *reinterpret_cast<uint2 *>(&sm_q[n][e0 * 2 + 8 * i]) = make_uint2(w[2 * i], w[2 * i + 1]);
+      if ((tid & 15) == 0) sm_qf[n] = factor;
+    }
+    __syncthreads();
+
+    const int64_t row_bytes = (int64_t)a.kv * S::kRowBytes;
+    const uint8_t *kbase = (const uint8_t *)a.kp.codes + (int64_t)h * S::kRowBytes + t * 16;
+    const uint8_t *vbase = (const uint8_t *)a.vp.codes + (int64_t)h * S::kRowBytes + g * S::kVBytes;
+    const float qf0 = sm_qf[2 * t], qf1 = sm_qf[2 * t + 1];
+    const int key_end = min(len, (blk0 + nseg) * S::kBlock);
+    const int key_0 = blk0 * S::kBlock + warp * S::kKeys;
+    constexpr int kRowRegs = (S::kKeys + 31) / 32;
+
+    float o[S::kMTiles][4];
+#pragma unroll
+    for (int i = 0; i < S::kMTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    float w0 = -INFINITY, w1 = -INFINITY;  // 8-bit codes: running maximum of s + log2(value scale)
+
+    // rows[]: lane i holds the pool row of the step's key i (32 + i), -1 where there is none
+    auto find_rows = [&](int key, int (&rows)[kRowRegs]) {
+#pragma unroll
+      for (int r = 0; r < kRowRegs; ++r) {
+        const int i = r * 32 + lane, p = key + i;
+        rows[r] = -1;
+        if (i < S::kKeys && p < key_end && (!a.mask || a.mask[(int64_t)b * a.mask_len + p]))
+          rows[r] = cache_row(a.pt, b, p);
+      }
+    };
+    auto row_of = [&](const int (&rows)[kRowRegs], int u, int i) {
+      return __shfl_sync(kFull, rows[(u * 16) / 32], (u * 16) % 32 + i);
+    };
+    uint32_t kc[S::kTiles][2][S::kKChunks][4];
+    float ks[kRowRegs];
+    auto load_k = [&](const int (&rows)[kRowRegs]) {
+#pragma unroll
+      for (int u = 0; u < S::kTiles; ++u)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int row = row_of(rows, u, half * 8 + g);
+          const uint8_t *p = kbase + row * row_bytes;
+#pragma unroll
+          for (int i = 0; i < S::kKChunks; ++i) load_codes<4>(kc[u][half][i], p + i * 64, row >= 0);
+        }
+      if constexpr (C::kScaled)
+#pragma unroll
+        for (int r = 0; r < kRowRegs; ++r) ks[r] = rows[r] >= 0 ? a.kp.scale[(int64_t)rows[r] * a.kv + h] : 0.0f;
+    };
+
+    int rows[kRowRegs], next[kRowRegs];
+    find_rows(key_0, rows);
+    load_k(rows);
+    find_rows(key_0 + S::kBlock, next);
+    for (int key = key_0; key < key_end; key += S::kBlock) {
+      // values of this step: on their way while the scores are formed
+      uint32_t vc[S::kTiles][4][S::kVChunks][S::kVBytes / 4];
+      float vs[kRowRegs];
+#pragma unroll
+      for (int u = 0; u < S::kTiles; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = row_of(rows, u, 2 * t + (i & 1) + (i >> 1) * 8);
+          const uint8_t *p = vbase + row * row_bytes;
+#pragma unroll
+          for (int j = 0; j < S::kVChunks; ++j) load_codes<S::kVBytes / 4>(vc[u][i][j], p + j * 8 * S::kVBytes, row >= 0);
+        }
+      if constexpr (C::kScaled)
+#pragma unroll
+        for (int r = 0; r < kRowRegs; ++r) vs[r] = rows[r] >= 0 ? a.vp.scale[(int64_t)rows[r] * a.kv + h] : 0.0f;
+      int after[kRowRegs];
+      find_rows(key + 2 * S::kBlock, after);
+
+      // S^T = K Q^T: rows (keys) g and g + 8, columns (heads) 2t and 2t + 1
+      float s[S::kTiles][4];
+#pragma unroll
+      for (int u = 0; u < S::kTiles; ++u) {
+        float x[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};  // two chains
+        if constexpr (C::kScaled) {
+#pragma unroll
+          for (int i = 0; i < S::kKChunks; ++i) {
+            uint32_t qb[8];
+            const uint8_t *qp = &sm_q[g][i * 128 + t * 32];
+            *reinterpret_cast<uint4 *>(&qb[0]) = *reinterpret_cast<const uint4 *>(qp);
+            *reinterpret_cast<uint4 *>(&qb[4]) = *reinterpret_cast<const uint4 *>(qp + 16);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              uint32_t a0, a1, a2, a3;
+              C::halves(kc[u][0][i][r], a0, a2);
+              C::halves(kc[u][1][i][r], a1, a3);
+              C::mma(x[r & 1], a0, a1, a2, a3, qb[2 * r], qb[2 * r + 1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < S::kKChunks; ++i) {
+            uint32_t qb[4];
+            *reinterpret_cast<uint4 *>(&qb[0]) = *reinterpret_cast<const uint4 *>(&sm_q[g][i * 64 + t * 16]);
+            C::mma(x[0], kc[u][0][i][0], kc[u][1][i][0], kc[u][0][i][1], kc[u][1][i][1], qb[0], qb[1]);
+            C::mma(x[1], kc[u][0][i][2], kc[u][1][i][2], kc[u][0][i][3], kc[u][1][i][3], qb[2], qb[3]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[u][i] = (x[0][i] + x[1][i]) * ((i & 1) ? qf1 : qf0);
+        const int ra = row_of(rows, u, g), rb = row_of(rows, u, 8 + g);
+        if constexpr (C::kScaled) {
+          const float ka = __shfl_sync(kFull, ks[(u * 16) / 32], (u * 16) % 32 + g);
+          const float kb = __shfl_sync(kFull, ks[(u * 16) / 32], (u * 16) % 32 + 8 + g);
+          s[u][0] *= ka, s[u][1] *= ka, s[u][2] *= kb, s[u][3] *= kb;
+        }
+        if (ra < 0) s[u][0] = s[u][1] = -INFINITY;
+        if (rb < 0) s[u][2] = s[u][3] = -INFINITY;
+      }
+      load_k(next);  // past the last step every row is -1: nothing is read
+
+      // online softmax: columns are heads, so a lane's two factors serve its scores and its sums
+      float n0 = m0, n1 = m1;
+#pragma unroll
+      for (int u = 0; u < S::kTiles; ++u) {
+        n0 = fmaxf(n0, fmaxf(s[u][0], s[u][2]));
+        n1 = fmaxf(n1, fmaxf(s[u][1], s[u][3]));
+      }
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, d));
+        n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, d));
+      }
+      const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
+      float f0 = ex2_approx(m0 - z0), f1 = ex2_approx(m1 - z1);
+      l0 *= f0, l1 *= f1;
+      m0 = n0, m1 = n1;
+      float p[S::kTiles][4];
+#pragma unroll
+      for (int u = 0; u < S::kTiles; ++u) {
+        p[u][0] = ex2_approx(s[u][0] - z0), p[u][2] = ex2_approx(s[u][2] - z0);
+        p[u][1] = ex2_approx(s[u][1] - z1), p[u][3] = ex2_approx(s[u][3] - z1);
+        l0 += p[u][0] + p[u][2];
+        l1 += p[u][1] + p[u][3];
+      }
+      if constexpr (C::kScaled) {
+        // A value's scale goes into its weight: 2^(s + log2 scale - w) with a maximum w of its
+        // own, which keeps the fp16 weights in range whatever the scales are.
+        float e0 = w0, e1 = w1;
+#pragma unroll
+        for (int u = 0; u < S::kTiles; ++u) {
+          const float va = log2_approx(__shfl_sync(kFull, vs[(u * 16) / 32], (u * 16) % 32 + g));
+          const float vb = log2_approx(__shfl_sync(kFull, vs[(u * 16) / 32], (u * 16) % 32 + 8 + g));
+          s[u][0] += va, s[u][1] += va, s[u][2] += vb, s[u][3] += vb;
+          e0 = fmaxf(e0, fmaxf(s[u][0], s[u][2]));
+          e1 = fmaxf(e1, fmaxf(s[u][1], s[u][3]));
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          e0 = fmaxf(e0, __shfl_xor_sync(kFull, e0, d));
+          e1 = fmaxf(e1, __shfl_xor_sync(kFull, e1, d));
+        }
+        const float y0 = e0 == -INFINITY ? 0.0f : e0, y1 = e1 == -INFINITY ? 0.0f : e1;
+        f0 = ex2_approx(w0 - y0), f1 = ex2_approx(w1 - y1);
+        w0 = e0, w1 = e1;
+#pragma unroll
+        for (int u = 0; u < S::kTiles; ++u) {
+          p[u][0] = ex2_approx(s[u][0] - y0), p[u][2] = ex2_approx(s[u][2] - y0);
+          p[u][1] = ex2_approx(s[u][1] - y1), p[u][3] = ex2_approx(s[u][3] - y1);
+        }
+      }
+      if (__any_sync(kFull, !(f0 == 1.0f && f1 == 1.0f))) {
+#pragma unroll
+        for (int i = 0; i < S::kMTiles; ++i) o[i][0] *= f0, o[i][1] *= f1, o[i][2] *= f0, o[i][3] *= f1;
+      }
+
+      // O^T += V^T P^T: the scores' layout, transposed 8 x 8, is the operand's
+#pragma unroll
+      for (int u = 0; u < S::kTiles; ++u) {
+        const uint32_t b0 = transpose8x8(C::pack(p[u][0], p[u][1]));
+        const uint32_t b1 = transpose8x8(C::pack(p[u][2], p[u][3]));
+#pragma unroll
+        for (int j = 0; j < S::kVChunks; ++j)
+#pragma unroll
+          for (int x = 0; x < S::kVBytes / 4; ++x) {
+            const uint32_t v0 = vc[u][0][j][x], v1 = vc[u][1][j][x], v2 = vc[u][2][j][x], v3 = vc[u][3][j][x];
+            if constexpr (C::kScaled) {
+              uint32_t a0, a1, a2, a3;
+              const int mt = j * (S::kVElems / 2) + 2 * x;
+              C::halves(prmt(v0, v1, 0x5140), a0, a1);
+              C::halves(prmt(v2, v3, 0x5140), a2, a3);
+              C::mma(o[mt], a0, a1, a2, a3, b0, b1);
+              C::halves(prmt(v0, v1, 0x7362), a0, a1);
+              C::halves(prmt(v2, v3, 0x7362), a2, a3);
+              C::mma(o[mt + 1], a0, a1, a2, a3, b0, b1);
+            } else {
+              C::mma(o[j * (S::kVElems / 2) + x], prmt(v0, v1, 0x5410), prmt(v0, v1, 0x7632), prmt(v2, v3, 0x5410),
+                     prmt(v2, v3, 0x7632), b0, b1);
+            }
+          }
+      }
+#pragma unroll
+      for (int r = 0; r < kRowRegs; ++r) rows[r] = next[r], next[r] = after[r];
+    }
+
+    // ---- the warps' sums together
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) {
+      l0 += __shfl_xor_sync(kFull, l0, d);
+      l1 += __shfl_xor_sync(kFull, l1, d);
+    }
+    if constexpr (C::kScaled) {  // from the weights' maximum back to the scores'
+      const float f0 = m0 == -INFINITY || w0 == -INFINITY ? 0.0f : ex2_approx(w0 - m0);
+      const float f1 = m1 == -INFINITY || w1 == -INFINITY ? 0.0f : ex2_approx(w1 - m1);
+#pragma unroll
+      for (int i = 0; i < S::kMTiles; ++i) o[i][0] *= f0, o[i][1] *= f1, o[i][2] *= f0, o[i][3] *= f1;
+    }
+    if (g == 0) {
+      sm_m[warp][2 * t] = m0, sm_m[warp][2 * t + 1] = m1;
+      sm_l[warp][2 * t] = l0, sm_l[warp][2 * t + 1] = l1;
+    }
+#pragma unroll
+    for (int i = 0; i < S::kMTiles; ++i) {
+      const int d = i / (S::kVElems / 2) * 8 * S::kVElems + g * S::kVElems + i % (S::kVElems / 2) * 2;
+      *reinterpret_cast<float2 *>(&sm_o[warp][2 * t][d]) = make_float2(o[i][0], o[i][2]);
+      *reinterpret_cast<float2 *>(&sm_o[warp][2 * t + 1][d]) = make_float2(o[i][1], o[i][3]);
+    }
+    __syncthreads();
+    const bool whole = nseg == nblk;
+    const int slot = 2 * blockIdx.x + (c > c0);
+    float *part = parts + (int64_t)slot * kPartFloats<D>;
+    for (int i = tid; i < nh * (D / 4); i += kWarps * 32) {
+      const int n = i / (D / 4), d = i % (D / 4) * 4;
+      float mm = sm_m[0][n];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, sm_m[w][n]);
+      float4 x = make_float4(0, 0, 0, 0);
+      float l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = sm_m[w][n] == -INFINITY ? 0.0f : ex2_approx(sm_m[w][n] - mm);
+        const float4 y = *reinterpret_cast<const float4 *>(&sm_o[w][n][d]);
+        x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+        l += f * sm_l[w][n];
+      }
+      if (whole) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t at_out = ((int64_t)b * a.heads + h0 + n);
+        *reinterpret_cast<uint2 *>(a.out + at_out * D + d) =
+            make_uint2(CodeBf16::pack(x.x * inv, x.y * inv), CodeBf16::pack(x.z * inv, x.w * inv));
+        if (d == 0 && a.lse) a.lse[at_out] = l == 0.0f ? -INFINITY : (mm + log2f(l)) * 0.6931471805599453f;
+      } else {
+        *reinterpret_cast<float4 *>(part + n * D + d) = x;
+        if (d == 0) part[kHeadsPerUnit * D + 2 * n] = mm, part[kHeadsPerUnit * D + 2 * n + 1] = l;
+      }
+    }
+    if (!whole && blk0 == 0 && tid == 0) {
+      info->unit = b * upb + ub;
+      info->last = (int)((c + nblk - 1) / share);
+      info->slot = slot;
+    }
+    __syncthreads();
+    c += nseg;
+    at += nseg;
+    if (at == (int64_t)nblk * upb) at = 0, ++b;
+  }
 }
 
-size_t attend_workspace(int, int, int, int, int, int, int) { return 0; }
+// Adds up the parts of the unit that starts in k_attend's CTA blockIdx.x and goes on in others,
+// for one of its heads: D/4 lanes a part, the groups of lanes taking turns.
+template <int D>
+__global__ void __launch_bounds__(512) k_attend_join(const __grid_constant__ AttendArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int kLanes = D / 4, kTurns = 512 / kLanes;
+  __shared__ __align__(16) float4 sm_x[kTurns][kLanes];
+  __shared__ float sm_w[512], sm_red[16];
+  const Part pt = reinterpret_cast<const Part *>(a.part)[blockIdx.x];
+  if (pt.unit < 0) return;
+  const float *parts = a.part + (gridDim.x * sizeof(Part) / 4 + 3) / 4 * 4;
+  const int n = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = a.heads / a.kv, groups = head_groups(a.heads, a.kv), upb = a.kv * groups;
+  const int b = pt.unit / upb, ub = pt.unit % upb, grp = ub % groups;
+  if (grp * kHeadsPerUnit + n >= group) return;
+  const int first = blockIdx.x, count = pt.last - first + 1;
+  auto part_of = [&](int i) { return parts + (int64_t)(i == 0 ? pt.slot : 2 * (first + i)) * kPartFloats<D>; };
+
+  float mm = -INFINITY;
+  for (int i = tid; i < count; i += 512) mm = fmaxf(mm, part_of(i)[kHeadsPerUnit * D + 2 * n]);
+  mm = warp_max(mm);
+  if (lane == 0) sm_red[warp] = mm;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 16; ++w) mm = fmaxf(mm, sm_red[w]);
+  __syncthreads();
+
+  float l = 0.0f;
+  float4 x = make_float4(0, 0, 0, 0);
+  const int turn = tid / kLanes, d4 = tid % kLanes;
+  for (int i0 = 0; i0 < count; i0 += 512) {
+    const int i = i0 + tid;
+    float w = 0.0f;
+    if (i < count) {
+      const float m = part_of(i)[kHeadsPerUnit * D + 2 * n];
+      w = m == -INFINITY ? 0.0f : ex2_approx(m - mm);
+      l += w * part_of(i)[kHeadsPerUnit * D + 2 * n + 1];
+    }
+    sm_w[tid] = w;
+    __syncthreads();
+    const int here = min(512, count - i0);
+#pragma unroll 8
+    for (int j = turn; j < here; j += kTurns) {
+      const float f = sm_w[j];
+      const float4 y = *reinterpret_cast<const float4 *>(part_of(i0 + j) + n * D + d4 * 4);
+      x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+    }
+    __syncthreads();
+  }
+  l = warp_sum(l);
+  if (lane == 0) sm_red[warp] = l;
+  sm_x[turn][d4] = x;
+  __syncthreads();
+  if (tid >= kLanes) return;
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) l += sm_red[w];
+#pragma unroll
+  for (int j = 1; j < kTurns; ++j) {
+    const float4 y = sm_x[j][tid];
+    x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int64_t at = (int64_t)b * a.heads + (ub / groups) * group + grp * kHeadsPerUnit + n;
+  *reinterpret_cast<uint2 *>(a.out + at * D + tid * 4) =
+      make_uint2(CodeBf16::pack(x.x * inv, x.y * inv), CodeBf16::pack(x.z * inv, x.w * inv));
+  if (tid == 0 && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (mm + log2f(l)) * 0.6931471805599453f;
+}
 
 namespace {
+
+// CTAs of a call: as many as are resident at once, or the blocks of keys there can be.
+template <typename C, int D>
+int attend_grid(int B, int heads, int kv, int page_size, int max_pages) {
+  using S = Shape<C, D>;
+  const int64_t cap = (int64_t)page_size * max_pages;
+  const int64_t most = (int64_t)B * kv * head_groups(heads, kv) * ((cap + S::kBlock - 1) / S::kBlock);
+  const int64_t resident = (int64_t)148 * S::kBlocksPerSm;
+  return (int)(most < resident ? most : resident);
+}
+template <typename C, int D>
+size_t attend_bytes(int B, int heads, int kv, int page_size, int max_pages) {
+  const size_t grid = attend_grid<C, D>(B, heads, kv, page_size, max_pages);
+  return (grid * sizeof(Part) / 4 + 3) / 4 * 16 + grid * 2 * kPartFloats<D> * 4;
+}
 template <typename C, int D>
 cudaError_t attend_go(const AttendArgs &a, cudaStream_t s) {
-  return launch_pdl(k_attend<C, D>, dim3(a.heads, a.B), kWarps * 32, 0, s, a);
+  const int grid = attend_grid<C, D>(a.B, a.heads, a.kv, a.pt.page_size, a.pt.max_pages);
+  const cudaError_t e = launch_pdl(k_attend<C, D>, dim3(grid), kWarps * 32, 0, s, a);
+  const int group = a.heads / a.kv;
+  if (e != cudaSuccess || grid == 1) return e;
+  return launch_pdl(k_attend_join<D>, dim3(grid, group < kHeadsPerUnit ? group : kHeadsPerUnit), 512, 0, s, a);
 }
-template <typename C>
-cudaError_t attend_dim(const AttendArgs &a, int head_dim, cudaStream_t s) {
-  return head_dim == 64 ? attend_go<C, 64>(a, s) : head_dim == 128 ? attend_go<C, 128>(a, s) : attend_go<C, 256>(a, s);
-}
+
+#define PI0X_PICK(fn, dtype, dim, ...)                                                                      \
+  auto by_dim = [&](auto c) {                                                                               \
+    using C = decltype(c);                                                                                  \
+    return (dim) == 64 ? fn<C, 64>(__VA_ARGS__) : (dim) == 128 ? fn<C, 128>(__VA_ARGS__) : fn<C, 256>(__VA_ARGS__); \
+  };                                                                                                        \
+  return (dtype) == PI0X_DTYPE_E4M3 ? by_dim(CodeE4m3()) : (dtype) == PI0X_DTYPE_INT8 ? by_dim(CodeInt8()) : by_dim(CodeBf16())
+
 }  // namespace
 
+size_t attend_workspace(int B, int heads, int kv, int head_dim, int pool_dtype, int page_size, int max_pages) {
+  PI0X_PICK(attend_bytes, pool_dtype, head_dim, B, heads, kv, page_size, max_pages);
+}
 cudaError_t launch_attend(const AttendArgs &a, int pool_dtype, int head_dim, cudaStream_t s) {
-  return pool_dtype == PI0X_DTYPE_E4M3   ? attend_dim<__nv_fp8_e4m3>(a, head_dim, s)
-         : pool_dtype == PI0X_DTYPE_INT8 ? attend_dim<int8_t>(a, head_dim, s)
-                                         : attend_dim<bf16>(a, head_dim, s);
+  PI0X_PICK(attend_go, pool_dtype, head_dim, a, s);
 }
 
 }  // namespace pi0x
