@@ -28,24 +28,16 @@ constexpr int kWarps = 4;
 constexpr int kHeadsPerUnit = 8;  // query heads of one kv head that share a pass: the product's columns
 constexpr unsigned kFull = 0xffffffffu;
 
-// 16 or 8 bytes of a row into registers, zeros where there is no row.  Read once: not kept in L1.
+// 16 or 8 bytes of a row into registers.  Read once: not kept in L1.
 template <int N>
-__device__ __forceinline__ void load_codes(uint32_t (&r)[N], const void *p, bool valid) {
+__device__ __forceinline__ void load_codes(uint32_t (&r)[N], const void *p) {
   if constexpr (N == 4)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-        "@p ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3])
-        : "l"(p), "r"((int)valid)
-        : "memory");
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "l"(p)
+                 : "memory");
   else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
-        "@p ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];\n\t}"
-        : "=&r"(r[0]), "=&r"(r[1])
-        : "l"(p), "r"((int)valid)
-        : "memory");
+    asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p) : "memory");
 }
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
 // The 8x8 matrix of 16-bit elements spread over the warp, transposed.
@@ -53,6 +45,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
+}
+// What the lane that keeps key i of 16-key tile u holds.
+template <typename V, int N>
+__device__ __forceinline__ V of_key(const V (&v)[N], int u, int i) {
+  return __shfl_sync(kFull, v[(u * 16) / 32], (u * 16) % 32 + i);
 }
 __device__ __forceinline__ float log2_approx(float x) {
   float y;
@@ -119,14 +116,14 @@ struct Shape {
   static constexpr int kVBytes = kRowBytes >= 128 ? 16 : 8;             // bytes of a value a lane loads at once
   static constexpr int kVChunks = kRowBytes / (8 * kVBytes);
   static constexpr int kVElems = kVBytes / C::kBytes;
-  // keys a warp takes at once: 16 per product, more where rows are short, so that up to 4 KB
-  // of keys are on their way (8 KB at 512 bytes a row)
-  static constexpr int kTiles = kRowBytes >= 256 ? 1 : 256 / kRowBytes;
+  // keys a warp takes at once: 16 per product, more where rows are short, so that up to 8 KB
+  // of keys are on their way
+  static constexpr int kTiles = kRowBytes >= 512 ? 1 : kRowBytes >= 256 ? 2 : 4;
   static constexpr int kKeys = 16 * kTiles;
   static constexpr int kBlock = kWarps * kKeys;                         // keys of a scheduling block
   static constexpr int kMTiles = D / 16;
   static constexpr int kQPad = C::kBytes == 2 ? 64 : 16;                // bytes: keeps 8 heads' reads apart in the banks
-  static constexpr int kBlocksPerSm = kRowBytes >= 512 ? 2 : 3;
+  static constexpr int kBlocksPerSm = 2;
 };
 
 // Work: units u = (sample, kv head, group of up to 8 query heads), each of ceil(len/kBlock)
@@ -134,10 +131,24 @@ struct Shape {
 // takes `share` consecutive blocks, whichever units they belong to.  A unit inside one CTA is
 // finished there; of a longer one every CTA leaves its part (m, l and the unnormalised sum) in
 // the workspace, and k_attend_join adds them up in order.
-struct Part {
-  int unit;    // unit this CTA is the first of several CTAs of, or -1
-  int last;    // its last CTA
-  int slot;    // part of the first CTA; CTA c > first: part 2c
+template <int N>
+struct Look {
+  int page[N];
+  uint8_t on[N];
+};
+template <int N>
+struct Step {
+  int rows[N];
+  unsigned seen[N];
+  bool any;
+};
+//
+// Split units are listed in the workspace: by unit if there are no more units than CTAs,
+// else by the CTA that a unit starts in (each CTA starts at most one that goes on).
+struct __align__(16) Split {
+  int unit;         // -1: none here
+  int first, last;  // its CTAs
+  int slot;         // the first CTA's part; that of CTA c > first is 2c
 };
 
 __device__ __forceinline__ int keys_of(const AttendArgs &a, int b) {
@@ -162,7 +173,6 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_atte
   __shared__ __align__(16) uint8_t sm_q[kHeadsPerUnit][D * 2 + S::kQPad];
   __shared__ float sm_m[kWarps][kHeadsPerUnit], sm_l[kWarps][kHeadsPerUnit], sm_qf[kHeadsPerUnit];
   __shared__ int sm_scan[kWarps], sm_b, sm_at;
-  __shared__ int sm_total;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int group = a.heads / a.kv, groups = head_groups(a.heads, a.kv), upb = a.kv * groups;
 
@@ -188,9 +198,10 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_atte
   const int64_t total = (int64_t)total_b * upb;
   const int64_t share = (total + gridDim.x - 1) / gridDim.x;
   const int64_t c0 = min(total, blockIdx.x * share), c1 = min(total, c0 + share);
-  Part *info = reinterpret_cast<Part *>(a.part) + blockIdx.x;
-  float *parts = a.part + (gridDim.x * sizeof(Part) / 4 + 3) / 4 * 4;
-  if (tid == 0) info->unit = -1;
+  Split *splits = reinterpret_cast<Split *>(a.part);
+  float *parts = a.part + gridDim.x * (sizeof(Split) / 4);
+  const bool by_unit = (int64_t)a.B * upb <= gridDim.x;
+  if (!by_unit && tid == 0) splits[blockIdx.x].unit = -1;
   {
     int64_t off = (int64_t)(before + incl - mine) * upb;
     if (c0 < c1 && c0 >= off && c0 < off + (int64_t)mine * upb) {
@@ -260,7 +271,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_atte
     const float qf0 = sm_qf[2 * t], qf1 = sm_qf[2 * t + 1];
     const int key_end = min(len, (blk0 + nseg) * S::kBlock);
     const int key_0 = blk0 * S::kBlock + warp * S::kKeys;
-    constexpr int kRowRegs = (S::kKeys + 31) / 32;
+    constexpr int kRegs = (S::kKeys + 31) / 32;  // a lane keeps key i of a step, and key 32 + i of longer ones
 
     float o[S::kMTiles][4];
 #pragma unroll
@@ -268,183 +279,205 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_atte
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
     float w0 = -INFINITY, w1 = -INFINITY;  // 8-bit codes: running maximum of s + log2(value scale)
 
-    // rows[]: lane i holds the pool row of the step's key i (32 + i), -1 where there is none
-    auto find_rows = [&](int key, int (&rows)[kRowRegs]) {
+    // A step's keys.  look() issues the loads of page numbers and mask two steps ahead and
+    // settle(), a step later, takes what came: seen has a bit for each visible key, and rows
+    // their pool rows.  An unseen key takes the row of a seen one of the step (its scores are
+    // dropped), so that no load has a condition and nothing but visible rows is read, whose
+    // values may stand beside weights of zero; a step without a visible key reads nothing.
+    auto look = [&](int key) {
+      Look<kRegs> k;
 #pragma unroll
-      for (int r = 0; r < kRowRegs; ++r) {
+      for (int r = 0; r < kRegs; ++r) {
         const int i = r * 32 + lane, p = key + i;
-        rows[r] = -1;
-        if (i < S::kKeys && p < key_end && (!a.mask || a.mask[(int64_t)b * a.mask_len + p]))
-          rows[r] = cache_row(a.pt, b, p);
+        const bool in = i < S::kKeys && p < key_end;
+        k.page[r] = -1;
+        k.on[r] = 1;
+        if (in) {
+          k.page[r] = a.pt.table[(int64_t)b * a.pt.max_pages + (uint32_t)p / (uint32_t)a.pt.page_size];
+          if (a.mask) k.on[r] = a.mask[(int64_t)b * a.mask_len + p];
+        }
       }
+      return k;
     };
-    auto row_of = [&](const int (&rows)[kRowRegs], int u, int i) {
-      return __shfl_sync(kFull, rows[(u * 16) / 32], (u * 16) % 32 + i);
+    auto settle = [&](const Look<kRegs> &k, int key) {
+      Step<kRegs> st;
+      int first = -1;
+#pragma unroll
+      for (int r = 0; r < kRegs; ++r) {
+        const bool ok = k.on[r] && k.page[r] >= 0 && k.page[r] < a.pt.num_pages;
+        st.rows[r] = k.page[r] * a.pt.page_size + (int)((uint32_t)(key + r * 32 + lane) % (uint32_t)a.pt.page_size);
+        st.seen[r] = __ballot_sync(kFull, ok);
+        if (first < 0 && st.seen[r]) first = __shfl_sync(kFull, st.rows[r], __ffs(st.seen[r]) - 1);
+      }
+      st.any = first >= 0;
+#pragma unroll
+      for (int r = 0; r < kRegs; ++r)
+        if (!(st.seen[r] >> lane & 1)) st.rows[r] = first;
+      return st;
     };
     uint32_t kc[S::kTiles][2][S::kKChunks][4];
-    float ks[kRowRegs];
-    auto load_k = [&](const int (&rows)[kRowRegs]) {
+    float ks[kRegs];
+    auto load_k = [&](const Step<kRegs> &st) {
 #pragma unroll
       for (int u = 0; u < S::kTiles; ++u)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const int row = row_of(rows, u, half * 8 + g);
-          const uint8_t *p = kbase + row * row_bytes;
+          const uint8_t *p = kbase + of_key(st.rows, u, half * 8 + g) * row_bytes;
 #pragma unroll
-          for (int i = 0; i < S::kKChunks; ++i) load_codes<4>(kc[u][half][i], p + i * 64, row >= 0);
+          for (int i = 0; i < S::kKChunks; ++i) load_codes<4>(kc[u][half][i], p + i * 64);
         }
       if constexpr (C::kScaled)
 #pragma unroll
-        for (int r = 0; r < kRowRegs; ++r) ks[r] = rows[r] >= 0 ? a.kp.scale[(int64_t)rows[r] * a.kv + h] : 0.0f;
+        for (int r = 0; r < kRegs; ++r) ks[r] = a.kp.scale[(int64_t)st.rows[r] * a.kv + h];
     };
 
-    int rows[kRowRegs], next[kRowRegs];
-    find_rows(key_0, rows);
-    load_k(rows);
-    find_rows(key_0 + S::kBlock, next);
+    Step<kRegs> now = settle(look(key_0), key_0);
+    if (now.any) load_k(now);
+    Look<kRegs> ahead = look(key_0 + S::kBlock);
     for (int key = key_0; key < key_end; key += S::kBlock) {
       // values of this step: on their way while the scores are formed
       uint32_t vc[S::kTiles][4][S::kVChunks][S::kVBytes / 4];
-      float vs[kRowRegs];
-#pragma unroll
-      for (int u = 0; u < S::kTiles; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = row_of(rows, u, 2 * t + (i & 1) + (i >> 1) * 8);
-          const uint8_t *p = vbase + row * row_bytes;
-#pragma unroll
-          for (int j = 0; j < S::kVChunks; ++j) load_codes<S::kVBytes / 4>(vc[u][i][j], p + j * 8 * S::kVBytes, row >= 0);
-        }
-      if constexpr (C::kScaled)
-#pragma unroll
-        for (int r = 0; r < kRowRegs; ++r) vs[r] = rows[r] >= 0 ? a.vp.scale[(int64_t)rows[r] * a.kv + h] : 0.0f;
-      int after[kRowRegs];
-      find_rows(key + 2 * S::kBlock, after);
-
-      // S^T = K Q^T: rows (keys) g and g + 8, columns (heads) 2t and 2t + 1
+      float vs[kRegs];
       float s[S::kTiles][4];
+      if (now.any) {
 #pragma unroll
-      for (int u = 0; u < S::kTiles; ++u) {
-        float x[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};  // two chains
-        if constexpr (C::kScaled) {
+        for (int u = 0; u < S::kTiles; ++u)
 #pragma unroll
-          for (int i = 0; i < S::kKChunks; ++i) {
-            uint32_t qb[8];
-            const uint8_t *qp = &sm_q[g][i * 128 + t * 32];
-            *reinterpret_cast<uint4 *>(&qb[0]) = *reinterpret_cast<const uint4 *>(qp);
-            *reinterpret_cast<uint4 *>(&qb[4]) = *reinterpret_cast<const uint4 *>(qp + 16);
+          for (int i = 0; i < 4; ++i) {
+            const uint8_t *p = vbase + of_key(now.rows, u, 2 * t + (i & 1) + (i >> 1) * 8) * row_bytes;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              uint32_t a0, a1, a2, a3;
-              C::halves(kc[u][0][i][r], a0, a2);
-              C::halves(kc[u][1][i][r], a1, a3);
-              C::mma(x[r & 1], a0, a1, a2, a3, qb[2 * r], qb[2 * r + 1]);
-            }
+            for (int j = 0; j < S::kVChunks; ++j) load_codes<S::kVBytes / 4>(vc[u][i][j], p + j * 8 * S::kVBytes);
           }
-        } else {
+        if constexpr (C::kScaled)
 #pragma unroll
-          for (int i = 0; i < S::kKChunks; ++i) {
-            uint32_t qb[4];
-            *reinterpret_cast<uint4 *>(&qb[0]) = *reinterpret_cast<const uint4 *>(&sm_q[g][i * 64 + t * 16]);
-            C::mma(x[0], kc[u][0][i][0], kc[u][1][i][0], kc[u][0][i][1], kc[u][1][i][1], qb[0], qb[1]);
-            C::mma(x[1], kc[u][0][i][2], kc[u][1][i][2], kc[u][0][i][3], kc[u][1][i][3], qb[2], qb[3]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[u][i] = (x[0][i] + x[1][i]) * ((i & 1) ? qf1 : qf0);
-        const int ra = row_of(rows, u, g), rb = row_of(rows, u, 8 + g);
-        if constexpr (C::kScaled) {
-          const float ka = __shfl_sync(kFull, ks[(u * 16) / 32], (u * 16) % 32 + g);
-          const float kb = __shfl_sync(kFull, ks[(u * 16) / 32], (u * 16) % 32 + 8 + g);
-          s[u][0] *= ka, s[u][1] *= ka, s[u][2] *= kb, s[u][3] *= kb;
-        }
-        if (ra < 0) s[u][0] = s[u][1] = -INFINITY;
-        if (rb < 0) s[u][2] = s[u][3] = -INFINITY;
-      }
-      load_k(next);  // past the last step every row is -1: nothing is read
+          for (int r = 0; r < kRegs; ++r) vs[r] = a.vp.scale[(int64_t)now.rows[r] * a.kv + h];
 
-      // online softmax: columns are heads, so a lane's two factors serve its scores and its sums
-      float n0 = m0, n1 = m1;
-#pragma unroll
-      for (int u = 0; u < S::kTiles; ++u) {
-        n0 = fmaxf(n0, fmaxf(s[u][0], s[u][2]));
-        n1 = fmaxf(n1, fmaxf(s[u][1], s[u][3]));
-      }
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) {
-        n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, d));
-        n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, d));
-      }
-      const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
-      float f0 = ex2_approx(m0 - z0), f1 = ex2_approx(m1 - z1);
-      l0 *= f0, l1 *= f1;
-      m0 = n0, m1 = n1;
-      float p[S::kTiles][4];
-#pragma unroll
-      for (int u = 0; u < S::kTiles; ++u) {
-        p[u][0] = ex2_approx(s[u][0] - z0), p[u][2] = ex2_approx(s[u][2] - z0);
-        p[u][1] = ex2_approx(s[u][1] - z1), p[u][3] = ex2_approx(s[u][3] - z1);
-        l0 += p[u][0] + p[u][2];
-        l1 += p[u][1] + p[u][3];
-      }
-      if constexpr (C::kScaled) {
-        // A value's scale goes into its weight: 2^(s + log2 scale - w) with a maximum w of its
-        // own, which keeps the fp16 weights in range whatever the scales are.
-        float e0 = w0, e1 = w1;
+        // S^T = K Q^T: rows (keys) g and g + 8, columns (heads) 2t and 2t + 1
 #pragma unroll
         for (int u = 0; u < S::kTiles; ++u) {
-          const float va = log2_approx(__shfl_sync(kFull, vs[(u * 16) / 32], (u * 16) % 32 + g));
-          const float vb = log2_approx(__shfl_sync(kFull, vs[(u * 16) / 32], (u * 16) % 32 + 8 + g));
-          s[u][0] += va, s[u][1] += va, s[u][2] += vb, s[u][3] += vb;
-          e0 = fmaxf(e0, fmaxf(s[u][0], s[u][2]));
-          e1 = fmaxf(e1, fmaxf(s[u][1], s[u][3]));
+          float x[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};  // two chains
+          if constexpr (C::kScaled) {
+#pragma unroll
+            for (int i = 0; i < S::kKChunks; ++i) {
+              uint32_t qb[8];
+              const uint8_t *qp = &sm_q[g][i * 128 + t * 32];
+              *reinterpret_cast<uint4 *>(&qb[0]) = *reinterpret_cast<const uint4 *>(qp);
+              *reinterpret_cast<uint4 *>(&qb[4]) = *reinterpret_cast<const uint4 *>(qp + 16);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                uint32_t a0, a1, a2, a3;
+                C::halves(kc[u][0][i][r], a0, a2);
+                C::halves(kc[u][1][i][r], a1, a3);
+                C::mma(x[r & 1], a0, a1, a2, a3, qb[2 * r], qb[2 * r + 1]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < S::kKChunks; ++i) {
+              uint32_t qb[4];
+              *reinterpret_cast<uint4 *>(&qb[0]) = *reinterpret_cast<const uint4 *>(&sm_q[g][i * 64 + t * 16]);
+              C::mma(x[0], kc[u][0][i][0], kc[u][1][i][0], kc[u][0][i][1], kc[u][1][i][1], qb[0], qb[1]);
+              C::mma(x[1], kc[u][0][i][2], kc[u][1][i][2], kc[u][0][i][3], kc[u][1][i][3], qb[2], qb[3]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[u][i] = (x[0][i] + x[1][i]) * ((i & 1) ? qf1 : qf0);
+          if constexpr (C::kScaled) {
+            const float ka = of_key(ks, u, g), kb = of_key(ks, u, 8 + g);
+            s[u][0] *= ka, s[u][1] *= ka, s[u][2] *= kb, s[u][3] *= kb;
+          }
+          const unsigned seen = now.seen[(u * 16) / 32] >> ((u * 16) % 32 + g);
+          if (!(seen & 1)) s[u][0] = s[u][1] = -INFINITY;
+          if (!(seen >> 8 & 1)) s[u][2] = s[u][3] = -INFINITY;
+        }
+      }
+      const Step<kRegs> coming = settle(ahead, key + S::kBlock);
+      ahead = look(key + 2 * S::kBlock);
+      if (coming.any) load_k(coming);
+      if (now.any) {
+        // online softmax: columns are heads, so a lane's two factors serve its scores and its sums
+        float n0 = m0, n1 = m1;
+#pragma unroll
+        for (int u = 0; u < S::kTiles; ++u) {
+          n0 = fmaxf(n0, fmaxf(s[u][0], s[u][2]));
+          n1 = fmaxf(n1, fmaxf(s[u][1], s[u][3]));
         }
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
-          e0 = fmaxf(e0, __shfl_xor_sync(kFull, e0, d));
-          e1 = fmaxf(e1, __shfl_xor_sync(kFull, e1, d));
+          n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, d));
+          n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, d));
         }
-        const float y0 = e0 == -INFINITY ? 0.0f : e0, y1 = e1 == -INFINITY ? 0.0f : e1;
-        f0 = ex2_approx(w0 - y0), f1 = ex2_approx(w1 - y1);
-        w0 = e0, w1 = e1;
+        const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
+        float f0 = ex2_approx(m0 - z0), f1 = ex2_approx(m1 - z1);
+        l0 *= f0, l1 *= f1;
+        m0 = n0, m1 = n1;
+        float p[S::kTiles][4];
 #pragma unroll
         for (int u = 0; u < S::kTiles; ++u) {
-          p[u][0] = ex2_approx(s[u][0] - y0), p[u][2] = ex2_approx(s[u][2] - y0);
-          p[u][1] = ex2_approx(s[u][1] - y1), p[u][3] = ex2_approx(s[u][3] - y1);
+          p[u][0] = ex2_approx(s[u][0] - z0), p[u][2] = ex2_approx(s[u][2] - z0);
+          p[u][1] = ex2_approx(s[u][1] - z1), p[u][3] = ex2_approx(s[u][3] - z1);
+          l0 += p[u][0] + p[u][2];
+          l1 += p[u][1] + p[u][3];
+        }
+        if constexpr (C::kScaled) {
+          // A value's scale goes into its weight: 2^(s + log2 scale - w) with a maximum w of its
+          // own, which keeps the fp16 weights in range whatever the scales are.
+          float e0 = w0, e1 = w1;
+#pragma unroll
+          for (int r = 0; r < kRegs; ++r) vs[r] = log2_approx(vs[r]);
+#pragma unroll
+          for (int u = 0; u < S::kTiles; ++u) {
+            const float va = of_key(vs, u, g), vb = of_key(vs, u, 8 + g);
+            s[u][0] += va, s[u][1] += va, s[u][2] += vb, s[u][3] += vb;
+            e0 = fmaxf(e0, fmaxf(s[u][0], s[u][2]));
+            e1 = fmaxf(e1, fmaxf(s[u][1], s[u][3]));
+          }
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            e0 = fmaxf(e0, __shfl_xor_sync(kFull, e0, d));
+            e1 = fmaxf(e1, __shfl_xor_sync(kFull, e1, d));
+          }
+          const float y0 = e0 == -INFINITY ? 0.0f : e0, y1 = e1 == -INFINITY ? 0.0f : e1;
+          f0 = ex2_approx(w0 - y0), f1 = ex2_approx(w1 - y1);
+          w0 = e0, w1 = e1;
+#pragma unroll
+          for (int u = 0; u < S::kTiles; ++u) {
+            p[u][0] = ex2_approx(s[u][0] - y0), p[u][2] = ex2_approx(s[u][2] - y0);
+            p[u][1] = ex2_approx(s[u][1] - y1), p[u][3] = ex2_approx(s[u][3] - y1);
+          }
+        }
+        if (__any_sync(kFull, !(f0 == 1.0f && f1 == 1.0f))) {
+#pragma unroll
+          for (int i = 0; i < S::kMTiles; ++i) o[i][0] *= f0, o[i][1] *= f1, o[i][2] *= f0, o[i][3] *= f1;
+        }
+
+        // O^T += V^T P^T: the scores' layout, transposed 8 x 8, is the operand's
+#pragma unroll
+        for (int u = 0; u < S::kTiles; ++u) {
+          const uint32_t b0 = transpose8x8(C::pack(p[u][0], p[u][1]));
+          const uint32_t b1 = transpose8x8(C::pack(p[u][2], p[u][3]));
+#pragma unroll
+          for (int j = 0; j < S::kVChunks; ++j)
+#pragma unroll
+            for (int x = 0; x < S::kVBytes / 4; ++x) {
+              const uint32_t v0 = vc[u][0][j][x], v1 = vc[u][1][j][x], v2 = vc[u][2][j][x], v3 = vc[u][3][j][x];
+              if constexpr (C::kScaled) {
+                uint32_t a0, a1, a2, a3;
+                const int mt = j * (S::kVElems / 2) + 2 * x;
+                C::halves(prmt(v0, v1, 0x5140), a0, a1);
+                C::halves(prmt(v2, v3, 0x5140), a2, a3);
+                C::mma(o[mt], a0, a1, a2, a3, b0, b1);
+                C::halves(prmt(v0, v1, 0x7362), a0, a1);
+                C::halves(prmt(v2, v3, 0x7362), a2, a3);
+                C::mma(o[mt + 1], a0, a1, a2, a3, b0, b1);
+              } else {
+                C::mma(o[j * (S::kVElems / 2) + x], prmt(v0, v1, 0x5410), prmt(v0, v1, 0x7632), prmt(v2, v3, 0x5410),
+                       prmt(v2, v3, 0x7632), b0, b1);
+              }
+            }
         }
       }
-      if (__any_sync(kFull, !(f0 == 1.0f && f1 == 1.0f))) {
-#pragma unroll
-        for (int i = 0; i < S::kMTiles; ++i) o[i][0] *= f0, o[i][1] *= f1, o[i][2] *= f0, o[i][3] *= f1;
-      }
-
-      // O^T += V^T P^T: the scores' layout, transposed 8 x 8, is the operand's
-#pragma unroll
-      for (int u = 0; u < S::kTiles; ++u) {
-        const uint32_t b0 = transpose8x8(C::pack(p[u][0], p[u][1]));
-        const uint32_t b1 = transpose8x8(C::pack(p[u][2], p[u][3]));
-#pragma unroll
-        for (int j = 0; j < S::kVChunks; ++j)
-#pragma unroll
-          for (int x = 0; x < S::kVBytes / 4; ++x) {
-            const uint32_t v0 = vc[u][0][j][x], v1 = vc[u][1][j][x], v2 = vc[u][2][j][x], v3 = vc[u][3][j][x];
-            if constexpr (C::kScaled) {
-              uint32_t a0, a1, a2, a3;
-              const int mt = j * (S::kVElems / 2) + 2 * x;
-              C::halves(prmt(v0, v1, 0x5140), a0, a1);
-              C::halves(prmt(v2, v3, 0x5140), a2, a3);
-              C::mma(o[mt], a0, a1, a2, a3, b0, b1);
-              C::halves(prmt(v0, v1, 0x7362), a0, a1);
-              C::halves(prmt(v2, v3, 0x7362), a2, a3);
-              C::mma(o[mt + 1], a0, a1, a2, a3, b0, b1);
-            } else {
-              C::mma(o[j * (S::kVElems / 2) + x], prmt(v0, v1, 0x5410), prmt(v0, v1, 0x7632), prmt(v2, v3, 0x5410),
-                     prmt(v2, v3, 0x7632), b0, b1);
-            }
-          }
-      }
-#pragma unroll
-      for (int r = 0; r < kRowRegs; ++r) rows[r] = next[r], next[r] = after[r];
+      now = coming;
     }
 
     // ---- the warps' sums together
@@ -471,7 +504,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_atte
     }
     __syncthreads();
     const bool whole = nseg == nblk;
-    const int slot = 2 * blockIdx.x + (c > c0);
+    const int slot = 2 * (int)blockIdx.x + (c > c0);
     float *part = parts + (int64_t)slot * kPartFloats<D>;
     for (int i = tid; i < nh * (D / 4); i += kWarps * 32) {
       const int n = i / (D / 4), d = i % (D / 4) * 4;
@@ -498,10 +531,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_atte
         if (d == 0) part[kHeadsPerUnit * D + 2 * n] = mm, part[kHeadsPerUnit * D + 2 * n + 1] = l;
       }
     }
-    if (!whole && blk0 == 0 && tid == 0) {
-      info->unit = b * upb + ub;
-      info->last = (int)((c + nblk - 1) / share);
-      info->slot = slot;
+    if (blk0 == 0 && tid == 0) {
+      const int unit = b * upb + ub;
+      if (!whole)
+        splits[by_unit ? unit : blockIdx.x] = Split{unit, (int)blockIdx.x, (int)((c + nblk - 1) / share), slot};
+      else if (by_unit && gridDim.x > 1)  // a lone CTA has no workspace and no second kernel
+        splits[unit].unit = -1;
     }
     __syncthreads();
     c += nseg;
@@ -510,74 +545,97 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_atte
   }
 }
 
-// Adds up the parts of the unit that starts in k_attend's CTA blockIdx.x and goes on in others,
-// for one of its heads: D/4 lanes a part, the groups of lanes taking turns.
+// Adds up the parts of split unit blockIdx.x, in order of the keys.  A part is 8 heads x D/4
+// vectors; blockIdx.y takes an equal share of them, so that a few units with hundreds of
+// parts spread over many SMs.  Threads beyond a share's vectors take turns at the parts.
 template <int D>
-__global__ void __launch_bounds__(512) k_attend_join(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(256) k_attend_join(const __grid_constant__ AttendArgs a, int grid) {
   pdl_wait();
   pdl_trigger();
-  constexpr int kLanes = D / 4, kTurns = 512 / kLanes;
-  __shared__ __align__(16) float4 sm_x[kTurns][kLanes];
-  __shared__ float sm_w[512], sm_red[16];
-  const Part pt = reinterpret_cast<const Part *>(a.part)[blockIdx.x];
-  if (pt.unit < 0) return;
-  const float *parts = a.part + (gridDim.x * sizeof(Part) / 4 + 3) / 4 * 4;
-  const int n = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kChunk = 32, kAhead = 4, kStats = kHeadsPerUnit * D;
+  __shared__ float sm_w[kChunk][kHeadsPerUnit], sm_max[8][kHeadsPerUnit], sm_sum[8][kHeadsPerUnit];
+  __shared__ float4 sm_x[256];
+  const Split sp = reinterpret_cast<const Split *>(a.part)[blockIdx.x];
+  if (sp.unit < 0) return;
+  const float *parts = a.part + grid * (sizeof(Split) / 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = a.heads / a.kv, groups = head_groups(a.heads, a.kv), upb = a.kv * groups;
-  const int b = pt.unit / upb, ub = pt.unit % upb, grp = ub % groups;
-  if (grp * kHeadsPerUnit + n >= group) return;
-  const int first = blockIdx.x, count = pt.last - first + 1;
-  auto part_of = [&](int i) { return parts + (int64_t)(i == 0 ? pt.slot : 2 * (first + i)) * kPartFloats<D>; };
+  const int b = sp.unit / upb, ub = sp.unit % upb, h0 = ub / groups * group + ub % groups * kHeadsPerUnit;
+  const int nh = min(kHeadsPerUnit, group - ub % groups * kHeadsPerUnit);
+  const int count = sp.last - sp.first + 1;
+  auto part_of = [&](int i) { return parts + (int64_t)(i == 0 ? sp.slot : 2 * (sp.first + i)) * kPartFloats<D>; };
 
-  float mm = -INFINITY;
-  for (int i = tid; i < count; i += 512) mm = fmaxf(mm, part_of(i)[kHeadsPerUnit * D + 2 * n]);
-  mm = warp_max(mm);
-  if (lane == 0) sm_red[warp] = mm;
-  __syncthreads();
+  const int share = 2 * D / gridDim.y, lanes = min(share, 256), turns = 256 / lanes, turn = tid / lanes;
+  const int n = tid & 7, i_of = tid >> 3;  // this thread's head and part of a chunk's statistics
+  for (int v0 = 0; v0 < share; v0 += lanes) {
+    const int v = blockIdx.y * share + v0 + tid % lanes, head = v / (D / 4);
+    const bool mine = head < nh;
+    float4 ahead[kAhead];  // on their way while the weights are formed
 #pragma unroll
-  for (int w = 0; w < 16; ++w) mm = fmaxf(mm, sm_red[w]);
-  __syncthreads();
-
-  float l = 0.0f;
-  float4 x = make_float4(0, 0, 0, 0);
-  const int turn = tid / kLanes, d4 = tid % kLanes;
-  for (int i0 = 0; i0 < count; i0 += 512) {
-    const int i = i0 + tid;
-    float w = 0.0f;
-    if (i < count) {
-      const float m = part_of(i)[kHeadsPerUnit * D + 2 * n];
-      w = m == -INFINITY ? 0.0f : ex2_approx(m - mm);
-      l += w * part_of(i)[kHeadsPerUnit * D + 2 * n + 1];
+    for (int q = 0; q < kAhead; ++q) {
+      const int j = turn + q * turns;
+      ahead[q] = make_float4(0, 0, 0, 0);
+      if (mine && j < min(count, kChunk)) ahead[q] = *reinterpret_cast<const float4 *>(part_of(j) + 4 * v);
     }
-    sm_w[tid] = w;
+    float mm = -INFINITY;
+    if (n < nh)
+      for (int i = i_of; i < count; i += kChunk) mm = fmaxf(mm, part_of(i)[kStats + 2 * n]);
+    mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, 8));
+    mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, 16));
+    if (lane < 8) sm_max[warp][n] = mm;
     __syncthreads();
-    const int here = min(512, count - i0);
-#pragma unroll 8
-    for (int j = turn; j < here; j += kTurns) {
-      const float f = sm_w[j];
-      const float4 y = *reinterpret_cast<const float4 *>(part_of(i0 + j) + n * D + d4 * 4);
-      x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) mm = fmaxf(mm, sm_max[w][n]);
+
+    float l = 0.0f;
+    float4 x = make_float4(0, 0, 0, 0);
+    auto add = [&](float f, const float4 &y) { x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w; };
+    for (int i0 = 0; i0 < count; i0 += kChunk) {
+      const int i = i0 + i_of;
+      float w = 0.0f;
+      if (n < nh && i < count) {
+        const float m = part_of(i)[kStats + 2 * n];
+        w = m == -INFINITY ? 0.0f : ex2_approx(m - mm);
+        l += w * part_of(i)[kStats + 2 * n + 1];
+      }
+      sm_w[i_of][n] = w;
+      __syncthreads();
+      const int here = min(kChunk, count - i0);
+      int j = turn;
+      if (i0 == 0) {
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q, j += turns)
+          if (j < here) add(sm_w[j][head], ahead[q]);
+      }
+      if (mine)
+#pragma unroll 4
+        for (; j < here; j += turns) add(sm_w[j][head], *reinterpret_cast<const float4 *>(part_of(i0 + j) + 4 * v));
+      __syncthreads();
+    }
+    l += __shfl_xor_sync(kFull, l, 8);
+    l += __shfl_xor_sync(kFull, l, 16);
+    if (lane < 8) sm_sum[warp][n] = l;
+    sm_x[tid] = x;
+    __syncthreads();
+    if (tid < lanes && mine) {
+      l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) l += sm_sum[w][head];
+      for (int j = 1; j < turns; ++j) add(1.0f, sm_x[j * lanes + tid]);
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const int64_t at = (int64_t)b * a.heads + h0 + head;
+      const int d = v % (D / 4) * 4;
+      *reinterpret_cast<uint2 *>(a.out + at * D + d) =
+          make_uint2(CodeBf16::pack(x.x * inv, x.y * inv), CodeBf16::pack(x.z * inv, x.w * inv));
+      if (d == 0 && a.lse) {
+        mm = sm_max[0][head];
+#pragma unroll
+        for (int w = 1; w < 8; ++w) mm = fmaxf(mm, sm_max[w][head]);
+        a.lse[at] = l == 0.0f ? -INFINITY : (mm + log2f(l)) * 0.6931471805599453f;
+      }
     }
     __syncthreads();
   }
-  l = warp_sum(l);
-  if (lane == 0) sm_red[warp] = l;
-  sm_x[turn][d4] = x;
-  __syncthreads();
-  if (tid >= kLanes) return;
-  l = 0.0f;
-#pragma unroll
-  for (int w = 0; w < 16; ++w) l += sm_red[w];
-#pragma unroll
-  for (int j = 1; j < kTurns; ++j) {
-    const float4 y = sm_x[j][tid];
-    x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-  }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const int64_t at = (int64_t)b * a.heads + (ub / groups) * group + grp * kHeadsPerUnit + n;
-  *reinterpret_cast<uint2 *>(a.out + at * D + tid * 4) =
-      make_uint2(CodeBf16::pack(x.x * inv, x.y * inv), CodeBf16::pack(x.z * inv, x.w * inv));
-  if (tid == 0 && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (mm + log2f(l)) * 0.6931471805599453f;
 }
 
 namespace {
@@ -594,15 +652,18 @@ int attend_grid(int B, int heads, int kv, int page_size, int max_pages) {
 template <typename C, int D>
 size_t attend_bytes(int B, int heads, int kv, int page_size, int max_pages) {
   const size_t grid = attend_grid<C, D>(B, heads, kv, page_size, max_pages);
-  return (grid * sizeof(Part) / 4 + 3) / 4 * 16 + grid * 2 * kPartFloats<D> * 4;
+  return grid > 1 ? grid * (sizeof(Split) + 2 * kPartFloats<D> * sizeof(float)) : 0;
 }
 template <typename C, int D>
 cudaError_t attend_go(const AttendArgs &a, cudaStream_t s) {
   const int grid = attend_grid<C, D>(a.B, a.heads, a.kv, a.pt.page_size, a.pt.max_pages);
   const cudaError_t e = launch_pdl(k_attend<C, D>, dim3(grid), kWarps * 32, 0, s, a);
-  const int group = a.heads / a.kv;
-  if (e != cudaSuccess || grid == 1) return e;
-  return launch_pdl(k_attend_join<D>, dim3(grid, group < kHeadsPerUnit ? group : kHeadsPerUnit), 512, 0, s, a);
+  if (e != cudaSuccess || grid == 1) return e;  // one CTA: nothing is split
+  const int64_t units = (int64_t)a.B * a.kv * head_groups(a.heads, a.kv);
+  const int lists = (int)(units < grid ? units : grid);
+  int shares = 1;  // about one CTA an SM in all, 16 vectors or more each
+  while (shares < D / 8 && lists * shares < 148) shares *= 2;
+  return launch_pdl(k_attend_join<D>, dim3(lists, shares), 256, 0, s, a, grid);
 }
 
 #define PI0X_PICK(fn, dtype, dim, ...)                                                                      \

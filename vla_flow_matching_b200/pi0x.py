@@ -12,6 +12,11 @@ from typing import Optional, Sequence
 
 import numpy as np
 
+try:
+    import torch
+except ImportError:  # the sampler itself takes numpy arrays
+    torch = None
+
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpi0x.so")
 
 PI0X_OK, PI0X_EINVAL, PI0X_EUNSUPPORTED, PI0X_ENOMEM, PI0X_ECUDA, PI0X_ETIMEOUT, PI0X_EDEVICE = range(7)
@@ -199,98 +204,79 @@ def attention_noalloc(q, ks, vs, prefix_k, prefix_v, mask, B, H, P, step0, out, 
     return out
 
 
-def _device_of(what: str, *tensors):
-    """The CUDA device that every given tensor (None: left out) lies on."""
-    device = None
+def _device_of(what: str, *tensors) -> int:
+    """Index of the CUDA device that every given tensor (None: left out) lies on."""
+    index = None
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{what}: every tensor must be on a CUDA device")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{what}: tensors on {device} and {t.device}")
-    return device
-
-
-class _on:
-    """Makes `device` current for the calls inside, and gives its current stream."""
-
-    def __init__(self, device):
-        import torch
-        self._guard = torch.cuda.device(device) if torch.cuda.current_device() != device.index else None
-        self._stream = torch.cuda.current_stream
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self._stream().cuda_stream
-
-    def __exit__(self, *e):
-        if self._guard is not None:
-            self._guard.__exit__(*e)
+        if t is not None:
+            i = t.get_device()
+            if i != index:
+                if i < 0:
+                    raise ValueError(f"{what}: every tensor must be on a CUDA device")
+                if index is not None:
+                    raise ValueError(f"{what}: tensors on cuda:{index} and cuda:{i}")
+                index = i
+    return index
 
 
 def _row_type(what: str, t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return PI0X_DTYPE_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return PI0X_DTYPE_F32
     raise ValueError(f"{what}: rows are bfloat16 or float32, not {t.dtype}")
 
 
-def _rows(what: str, t, B: int, T: int, dtype=None, head_dim=None) -> Rows:
-    """(B, T, heads, head_dim) tensor as strided rows."""
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != T or t.stride(3) != 1 or \
-            (head_dim is not None and t.shape[3] != head_dim) or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{what}: expected ({B}, {T}, heads, {head_dim or 'head_dim'}) rows of one type with a "
-                         f"contiguous last dimension, got {tuple(t.shape)} {t.dtype}")
-    s = t.stride()
-    return Rows(t.data_ptr(), s[0], s[1], s[2])
+def _rows(what: str, t, B: int, T: int, heads: int, D: int, dtype) -> Rows:
+    """(B, T, heads, D) tensor of `dtype` as strided rows."""
+    if t.shape != (B, T, heads, D) or t.dtype is not dtype:
+        raise ValueError(f"{what}: expected {(B, T, heads, D)} {dtype} rows, got {tuple(t.shape)} {t.dtype}")
+    sb, st, sh, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{what}: rows need a contiguous last dimension")
+    return Rows(t.data_ptr(), sb, st, sh)
+
+
+def _new_rows(t):
+    """A new contiguous tensor like `t`, and its rows."""
+    B, T, heads, D = t.shape
+    out = torch.empty_like(t, memory_format=torch.contiguous_format)
+    return out, Rows(out.data_ptr(), T * heads * D, heads * D, D)
 
 
 def _ints(what: str, name: str, t, *shape):
-    import torch
     if t is None:
         return 0
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: {name} must be a contiguous int32 tensor of shape {shape}")
     return t.data_ptr()
 
 
-def _bytes(what: str, name: str, t, B: int):
-    import torch
+def _mask(what: str, t, B: int):
+    """Pointer and length of a (B, length) mask (None: 0, 0)."""
     if t is None:
         return 0, 0
-    if t.dtype not in (torch.uint8, torch.bool) or t.dim() != 2 or t.shape[0] != B or t.shape[1] < 1 or \
-            not t.is_contiguous():
-        raise ValueError(f"{what}: {name} must be a contiguous uint8 or bool tensor of shape ({B}, 1 or more)")
+    if (t.dtype is not torch.uint8 and t.dtype is not torch.bool) or t.dim() != 2 or t.shape[0] != B or \
+            t.shape[1] < 1 or not t.is_contiguous():
+        raise ValueError(f"{what}: mask must be a contiguous uint8 or bool tensor of shape ({B}, 1 or more)")
     return t.data_ptr(), t.shape[1]
 
 
 def _gain(what: str, t, head_dim: int):
-    import torch
     if t is None:
         return 0
-    if t.dtype != torch.float32 or tuple(t.shape) != (head_dim,) or not t.is_contiguous():
+    if t.dtype is not torch.float32 or t.shape != (head_dim,) or not t.is_contiguous():
         raise ValueError(f"{what}: a gain is a contiguous float32 tensor of shape ({head_dim},)")
     return t.data_ptr()
 
 
-def _out(what: str, t, like):
-    """`t`, or a new tensor like `like` (its shape, contiguous)."""
-    import torch
-    if t is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    if t.dtype != like.dtype or t.shape != like.shape:
-        raise ValueError(f"{what}: an output must have its input's shape and type")
-    return t
+def _current_stream(index: int) -> int:
+    """torch's current stream on device `index`, as a handle."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def qk_norm_rope(q, k=None, start=None, *, positions=None, q_gain=None, k_gain=None, eps: float = 1e-6,
-                 rope_base: float = 10000.0, q_out=None, k_out=None):
+                 rope_base: Optional[float] = 10000.0, q_out=None, k_out=None):
     """Per-head RMSNorm (where a gain is given: gain 1 + g) and rotate-half rotation of
     queries and keys in one pass (pi0x_qk_norm_rope).
 
@@ -302,22 +288,35 @@ def qk_norm_rope(q, k=None, start=None, *, positions=None, q_gain=None, k_gain=N
     Runs on the current stream of the tensors' device.
     """
     what = "qk_norm_rope"
-    device = _device_of(what, q, k, start, positions, q_gain, k_gain, q_out, k_out)
+    index = _device_of(what, q, k, start, positions, q_gain, k_gain, q_out, k_out)
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return qk_norm_rope(q, k, start, positions=positions, q_gain=q_gain, k_gain=k_gain, eps=eps,
+                                rope_base=rope_base, q_out=q_out, k_out=k_out)
     dtype = _row_type(what, q)
-    B, T, heads, D = q.shape if q.dim() == 4 else (0, 0, 0, 0)
-    rq = _rows(what, q, B, T)
-    rk = _rows(what, k, B, T, q.dtype, D) if k is not None else None
-    with _on(device) as stream:
-        q_out = _out(what, q_out, q)
-        k_out = _out(what, k_out, k) if k is not None else None
-        rot = Rotation(_gain(what, q_gain, D), _gain(what, k_gain, D),
-                       _ints(what, "positions", positions, B, T), eps, rope_base or 0.0)
-        if q.numel() == 0:
-            return q_out, k_out
-        _check(load().pi0x_qk_norm_rope(
-            dtype, B, T, heads, k.shape[2] if k is not None else 0, D, rq, rk, _ints(what, "start", start, B), rot,
-            _rows(what, q_out, B, T), _rows(what, k_out, B, T) if k is not None else None, stream),
-            "pi0x_qk_norm_rope")
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError(f"{what}: q and k are (batch, tokens, heads, head_dim)")
+    B, T, heads, D = q.shape
+    kv = 0 if k is None else k.shape[2]
+    rq = _rows(what, q, B, T, heads, D, q.dtype)
+    rk = None if k is None else _rows(what, k, B, T, kv, D, q.dtype)
+    rot = Rotation(_gain(what, q_gain, D), _gain(what, k_gain, D), _ints(what, "positions", positions, B, T), eps,
+                   rope_base or 0.0)
+    first = _ints(what, "start", start, B)
+    if q_out is None:
+        q_out, rqo = _new_rows(q)
+    else:
+        rqo = _rows(what, q_out, B, T, heads, D, q.dtype)
+    rko = None
+    if k is not None:
+        if k_out is None:
+            k_out, rko = _new_rows(k)
+        else:
+            rko = _rows(what, k_out, B, T, kv, D, q.dtype)
+    if B * T * (heads + kv) == 0:
+        return q_out, k_out
+    _check(load().pi0x_qk_norm_rope(dtype, B, T, heads, kv, D, rq, rk, first, rot, rqo, rko, _current_stream(index)),
+           "pi0x_qk_norm_rope")
     return q_out, k_out
 
 
@@ -333,7 +332,6 @@ class KVCache:
     """
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        import torch
         types = {torch.bfloat16: PI0X_DTYPE_BF16, torch.float8_e4m3fn: PI0X_DTYPE_E4M3, torch.int8: PI0X_DTYPE_INT8}
         if k.dtype not in types or k.dtype != v.dtype or k.dim() != 5 or k.shape != v.shape or \
                 not k.is_contiguous() or not v.is_contiguous():
@@ -345,17 +343,18 @@ class KVCache:
         for s in (k_scale, v_scale):
             if s is not None and (s.dtype != torch.float32 or s.shape != k.shape[:4] or not s.is_contiguous()):
                 raise ValueError("KVCache: scales must be contiguous float32 (layers, num_pages, page_size, kv_heads)")
-        self.device = _device_of("KVCache", k, v, k_scale, v_scale)
+        self._index = _device_of("KVCache", k, v, k_scale, v_scale)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.layers, self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
+        self.device = k.device
         self._desc = Cache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), *k.shape, types[k.dtype])
         self._lib = load()
+        self._attend_bytes = {}  # workspace bytes by (batch, heads, max_pages)
 
     @classmethod
     def empty(cls, layers: int, num_pages: int, page_size: int, kv_heads: int = 1, head_dim: int = 256,
               dtype: str = "bf16", device="cuda"):
         """A cache of zeros; ``dtype`` "bf16", "e4m3" or "int8"."""
-        import torch
         types = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}
         if dtype not in types:
             raise ValueError(f"KVCache: dtype is one of {sorted(types)}")
@@ -365,16 +364,18 @@ class KVCache:
             pools += [torch.zeros(shape[:4], dtype=torch.float32, device=device) for _ in range(2)]
         return cls(*pools)
 
-    def _on(self, what: str, *tensors):
-        device = _device_of(what, *tensors)
-        if device != self.device:
-            raise ValueError(f"{what}: tensors on {device}, the cache on {self.device}")
-        return _on(device)
+    def _elsewhere(self, what: str, *tensors) -> bool:
+        """Checks that the tensors lie with the cache; True if another device is current."""
+        index = _device_of(what, *tensors)
+        if index != self._index:
+            raise ValueError(f"{what}: tensors on cuda:{index}, the cache on cuda:{self._index}")
+        return index != torch.cuda.current_device()
 
-    def _table(self, what: str, table):
-        if table.dim() != 2:
-            raise ValueError(f"{what}: table must be a contiguous int32 tensor (batch, max_pages)")
-        return _ints(what, "table", table, *table.shape)
+    def _pages(self, what: str, table, B: int):
+        """Pointer and width of the page table of B samples."""
+        if table.dtype is not torch.int32 or table.dim() != 2 or table.shape[0] != B or not table.is_contiguous():
+            raise ValueError(f"{what}: table must be a contiguous int32 tensor of shape ({B}, max_pages)")
+        return table.data_ptr(), table.shape[1]
 
     def write(self, layer: int, k, v, table, start, count=None, *, q=None, q_out=None, positions=None, q_gain=None,
               k_gain=None, eps: float = 1e-6, rope_base: Optional[float] = None):
@@ -387,32 +388,35 @@ class KVCache:
         Returns ``q_out`` (new unless given), or None without q.
         """
         what = "KVCache.write"
-        on = self._on(what, k, v, table, start, count, q, q_out, positions, q_gain, k_gain)
+        if self._elsewhere(what, k, v, table, start, count, q, q_out, positions, q_gain, k_gain):
+            with torch.cuda.device(self._index):
+                return self.write(layer, k, v, table, start, count, q=q, q_out=q_out, positions=positions,
+                                  q_gain=q_gain, k_gain=k_gain, eps=eps, rope_base=rope_base)
         dtype = _row_type(what, k)
+        if k.dim() != 4 or (q is not None and q.dim() != 4):
+            raise ValueError(f"{what}: q, k and v are (batch, tokens, heads, head_dim)")
         B, T = k.shape[:2]
-        D = self.head_dim
-        rk, rv = _rows(what, k, B, T, head_dim=D), _rows(what, v, B, T, k.dtype, D)
-        if k.shape[2] != self.kv_heads or v.shape[2] != self.kv_heads:
-            raise ValueError(f"{what}: k and v have {k.shape[2]} and {v.shape[2]} heads, the cache {self.kv_heads}")
-        if table.shape[0] != B:
-            raise ValueError(f"{what}: table has {table.shape[0]} samples, k has {B}")
-        rot = None
+        D, kv = self.head_dim, self.kv_heads
+        rk, rv = _rows(what, k, B, T, kv, D, k.dtype), _rows(what, v, B, T, kv, D, k.dtype)
+        pages, max_pages = self._pages(what, table, B)
+        if start is None:
+            raise ValueError(f"{what}: start is required")
+        first, n = _ints(what, "start", start, B), _ints(what, "count", count, B)
+        rot = rq = rqo = None
+        heads = 0
         if q is not None or rope_base or q_gain is not None or k_gain is not None:
             rot = Rotation(_gain(what, q_gain, D), _gain(what, k_gain, D),
                            _ints(what, "positions", positions, B, T), eps, rope_base or 0.0)
-        rq = _rows(what, q, B, T, k.dtype, D) if q is not None else None
-        if start is None:
-            raise ValueError(f"{what}: start is required")
-        with on as stream:
-            if q is not None:
-                q_out = _out(what, q_out, q)
-            if k.numel() == 0:
-                return q_out
-            _check(self._lib.pi0x_cache_write(
-                self._desc, layer, dtype, B, T, rk, rv, self._table(what, table), table.shape[1],
-                _ints(what, "start", start, B), _ints(what, "count", count, B), rot,
-                q.shape[2] if q is not None else 0, rq, _rows(what, q_out, B, T) if q is not None else None, stream),
-                "pi0x_cache_write")
+        if q is not None:
+            heads = q.shape[2]
+            rq = _rows(what, q, B, T, heads, D, k.dtype)
+            if q_out is None:
+                q_out, rqo = _new_rows(q)
+            else:
+                rqo = _rows(what, q_out, B, T, heads, D, k.dtype)
+        if B * T:
+            _check(self._lib.pi0x_cache_write(self._desc, layer, dtype, B, T, rk, rv, pages, max_pages, first, n, rot,
+                                              heads, rq, rqo, _current_stream(self._index)), "pi0x_cache_write")
         return q_out
 
     def read(self, table, lens, length: int, *, mask=None, layer0: int = 0, layers: Optional[int] = None, dtype=None,
@@ -423,31 +427,35 @@ class KVCache:
         that hold a key: below ``lens[b]``, on a page of the pool and, with ``mask`` (B,
         length), nonzero there.  The others come out as zeros (pi0x_cache_read).
         """
-        import torch
         what = "KVCache.read"
-        on = self._on(what, table, lens, mask, k_out, v_out, mask_out)
+        if self._elsewhere(what, table, lens, mask, k_out, v_out, mask_out):
+            with torch.cuda.device(self._index):
+                return self.read(table, lens, length, mask=mask, layer0=layer0, layers=layers, dtype=dtype,
+                                 k_out=k_out, v_out=v_out, mask_out=mask_out)
         B = table.shape[0]
+        pages, max_pages = self._pages(what, table, B)
+        keys = _ints(what, "lens", lens, B)
         n = self.layers - layer0 if layers is None else layers
+        if n < 0 or length < 0:
+            raise ValueError(f"{what}: {n} layers of {length} slots")
         dtype = dtype or torch.bfloat16
-        m, mask_len = _bytes(what, "mask", mask, B)
+        m, mask_len = _mask(what, mask, B)
         if mask is not None and mask_len != length:
             raise ValueError(f"{what}: mask covers {mask_len} slots, not {length}")
         shape = (n, B, self.kv_heads, length, self.head_dim)
-        with on as stream:
-            outs = []
-            for t, sh, dt in ((k_out, shape, dtype), (v_out, shape, dtype), (mask_out, (B, length), torch.uint8)):
-                if t is None:
-                    t = torch.empty(sh, dtype=dt, device=self.device)
-                elif tuple(t.shape) != sh or t.dtype != dt or not t.is_contiguous():
-                    raise ValueError(f"{what}: outputs must be contiguous {shape} {dtype} and ({B}, {length}) uint8")
-                outs.append(t)
-            k_out, v_out, mask_out = outs
-            if k_out.numel() == 0 and n >= 1:
-                return k_out, v_out, mask_out
-            _check(self._lib.pi0x_cache_read(
-                self._desc, layer0, n, B, length, self._table(what, table), table.shape[1],
-                _ints(what, "lens", lens, B), m, _row_type(what, k_out), k_out.data_ptr(), v_out.data_ptr(),
-                mask_out.data_ptr(), stream), "pi0x_cache_read")
+        outs = []
+        for t, sh, dt in ((k_out, shape, dtype), (v_out, shape, dtype), (mask_out, (B, length), torch.uint8)):
+            if t is None:
+                t = torch.empty(sh, dtype=dt, device=self.device)
+            elif t.shape != sh or t.dtype != dt or not t.is_contiguous():
+                raise ValueError(f"{what}: outputs must be contiguous {shape} {dtype} and ({B}, {length}) uint8")
+            outs.append(t)
+        k_out, v_out, mask_out = outs
+        code = _row_type(what, k_out)
+        if B * length:
+            _check(self._lib.pi0x_cache_read(self._desc, layer0, n, B, length, pages, max_pages, keys, m, code,
+                                             k_out.data_ptr(), v_out.data_ptr(), mask_out.data_ptr(),
+                                             _current_stream(self._index)), "pi0x_cache_read")
         return k_out, v_out, mask_out
 
     def attend(self, layer: int, q, table, lens, *, mask=None, scale: Optional[float] = None, out=None, lse=None):
@@ -458,33 +466,39 @@ class KVCache:
         head_dim ** -0.5.  Returns (out, lse): (B, heads, head_dim) bf16 and (B, heads)
         fp32, zeros and -inf for a sample without keys.
         """
-        import torch
         what = "KVCache.attend"
-        on = self._on(what, q, table, lens, mask, out, lse)
-        if q.dim() != 3 or q.dtype != torch.bfloat16 or q.shape[2] != self.head_dim or q.stride(2) != 1:
-            raise ValueError(f"{what}: q must be (batch, heads, {self.head_dim}) bfloat16 with a contiguous last "
-                             "dimension")
-        B, heads, D = q.shape
-        if table.shape[0] != B:
-            raise ValueError(f"{what}: table has {table.shape[0]} samples, q has {B}")
-        m, mask_len = _bytes(what, "mask", mask, B)
-        with on as stream:
-            if out is None:
-                out = torch.empty((B, heads, D), dtype=torch.bfloat16, device=self.device)
-            if lse is None:
-                lse = torch.empty((B, heads), dtype=torch.float32, device=self.device)
-            if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or \
-                    lse.shape != q.shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous():
-                raise ValueError(f"{what}: out must be contiguous like q, lse contiguous float32 ({B}, {heads})")
-            if q.numel() == 0:
-                return out, lse
-            need = self._lib.pi0x_cache_attention_workspace(self._desc, B, heads, table.shape[1])
-            work = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-            s = q.stride()
-            _check(self._lib.pi0x_cache_attention(
-                self._desc, layer, B, heads, Rows(q.data_ptr(), s[0], 0, s[1]), self._table(what, table),
-                table.shape[1], _ints(what, "lens", lens, B), m, mask_len, D ** -0.5 if scale is None else scale,
-                out.data_ptr(), lse.data_ptr(), _ptr(work), need, stream), "pi0x_cache_attention")
+        if self._elsewhere(what, q, table, lens, mask, out, lse):
+            with torch.cuda.device(self._index):
+                return self.attend(layer, q, table, lens, mask=mask, scale=scale, out=out, lse=lse)
+        D = self.head_dim
+        if q.dim() != 3 or q.dtype is not torch.bfloat16 or q.shape[2] != D or q.stride(2) != 1:
+            raise ValueError(f"{what}: q must be (batch, heads, {D}) bfloat16 with a contiguous last dimension")
+        B, heads, _ = q.shape
+        pages, max_pages = self._pages(what, table, B)
+        keys = _ints(what, "lens", lens, B)
+        m, mask_len = _mask(what, mask, B)
+        if out is None:
+            out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        elif out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous():
+            raise ValueError(f"{what}: out must be contiguous and like q")
+        if lse is None:
+            lse = torch.empty((B, heads), dtype=torch.float32, device=self.device)
+        elif lse.shape != (B, heads) or lse.dtype is not torch.float32 or not lse.is_contiguous():
+            raise ValueError(f"{what}: lse must be contiguous float32 ({B}, {heads})")
+        if B * heads == 0:
+            return out, lse
+        need = self._attend_bytes.get((B, heads, max_pages))
+        if need is None:
+            need = self._lib.pi0x_cache_attention_workspace(self._desc, B, heads, max_pages)
+            if len(self._attend_bytes) < 4096:
+                self._attend_bytes[B, heads, max_pages] = need
+        # a workspace of this call alone, from torch's allocator on the current stream
+        work = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+        sb, sh, _ = q.stride()
+        _check(self._lib.pi0x_cache_attention(
+            self._desc, layer, B, heads, Rows(q.data_ptr(), sb, 0, sh), pages, max_pages, keys, m, mask_len,
+            D ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(), work.data_ptr() if need else 0,
+            need, _current_stream(self._index)), "pi0x_cache_attention")
         return out, lse
 
 
@@ -551,11 +565,7 @@ class Sampler:
         pk = (ctypes.c_void_p * L)(*[_ptr(k) for k in prefix_k])
         pv = (ctypes.c_void_p * L)(*[_ptr(v) for v in prefix_v])
         if stream is None:
-            try:
-                import torch
-                stream = torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else 0
-            except ImportError:
-                stream = 0
+            stream = torch.cuda.current_stream().cuda_stream if torch and torch.cuda.is_available() else 0
         _check(self._lib.pi0x_sample(self._h, pk, pv, _ptr(mask), B, P, _ptr(state), _ptr(x1),
                                      int(num_steps), _ptr(x0), ctypes.c_void_p(stream)),
                "pi0x_sample")
@@ -566,18 +576,19 @@ class Sampler:
         :meth:`KVCache.read` reads them (pi0x_sample_cache).  Runs on the current stream
         of the cache's device."""
         what = "Sampler.sample_cache"
-        on = cache._on(what, table, lens, mask)
+        if cache._elsewhere(what, table, lens, mask):
+            with torch.cuda.device(cache._index):
+                return self.sample_cache(cache, table, lens, length, state, x1, num_steps, mask=mask, x0=x0)
         if x0 is None:
             x0 = x1.new_empty(x1.shape) if hasattr(x1, "new_empty") else np.empty_like(x1)
         B = int(table.shape[0])
-        m, mask_len = _bytes(what, "mask", mask, B)
+        pages, max_pages = cache._pages(what, table, B)
+        m, mask_len = _mask(what, mask, B)
         if mask is not None and mask_len != length:
             raise ValueError(f"{what}: mask covers {mask_len} slots, not {length}")
-        with on as stream:
-            _check(self._lib.pi0x_sample_cache(
-                self._h, cache._desc, B, length, cache._table(what, table), int(table.shape[1]),
-                _ints(what, "lens", lens, B), m, _ptr(state), _ptr(x1), int(num_steps), _ptr(x0), stream),
-                "pi0x_sample_cache")
+        _check(self._lib.pi0x_sample_cache(self._h, cache._desc, B, length, pages, max_pages,
+                                           _ints(what, "lens", lens, B), m, _ptr(state), _ptr(x1), int(num_steps),
+                                           _ptr(x0), _current_stream(cache._index)), "pi0x_sample_cache")
         return x0
 
     def set_variant(self, time_grid: int = PI0X_TIME_PI0, x_prediction: bool = False,
