@@ -7,14 +7,16 @@
 // kv head, at most 4 * heads / bytes-per-code operations a byte (16 for 8 heads in bf16),
 // far below the tensor cores' share, above what the FP32 pipes could do beside the loads.
 // So the products go to the tensor cores with the small side, the heads, as the 8
-// columns of m16n8k16: S^T = K Q^T takes 16 keys as rows, O^T = V^T P^T 16 dims.  With
-// these shapes both operands come straight from global memory into the registers that
-// the products read, with no shared memory between: a contraction may take its index in
-// any order, so a lane's 16 consecutive bytes of a key stand for whichever columns the
-// lane owns (q is read in the same order), and a product's rows may be any dims.
+// columns of m16n8k16: S^T = K Q^T takes 16 keys as rows, O^T = V^T P^T 16 dims, and the
+// scores' layout transposed 8 x 8 is the weights' layout.
 //
-// A warp holds a step of 16 or more keys in registers (up to 8 KB of K and 8 KB of V),
-// loads the next keys while it works, and needs no barrier until its keys end.
+// A warp works through steps of 16 to 64 keys on its own: it copies their rows, whole rows at
+// a time, into a ring of three buffers (K, V, K, ...) in shared memory and reads operands
+// from there, so that two or three buffers of 8 KB are on their way at any time - 130 to 200
+// KB an SM, above what HBM's latency needs - and no barrier stands between warps until their
+// keys end.  (Loads straight into the products' registers, without shared memory, measured
+// slower: 54 against XXX us for 2 x 100k-131k bf16 keys.  A lane's share of V^T is 16 bytes of
+// four different rows, so a request of 8 lanes covers 32-byte pieces of 4 rows.)
 #include "cache.cuh"
 #include "common.cuh"
 #include "kernels.cuh"
@@ -26,18 +28,22 @@ namespace pi0x {
 namespace {
 constexpr int kWarps = 4;
 constexpr int kHeadsPerUnit = 8;  // query heads of one kv head that share a pass: the product's columns
+constexpr int kBlocksPerSm = 2, kMaxGrid = 148 * kBlocksPerSm;
+constexpr int kJoinThreads = 512;
 constexpr unsigned kFull = 0xffffffffu;
 
-// 16 or 8 bytes of a row into registers.  Read once: not kept in L1.
-template <int N>
-__device__ __forceinline__ void load_codes(uint32_t (&r)[N], const void *p) {
-  if constexpr (N == 4)
-    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "l"(p)
-                 : "memory");
-  else
-    asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p) : "memory");
+// Four 8x8 matrices of 16-bit elements, lane i's address the row i % 8 of matrix i / 8.
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
 // The 8x8 matrix of 16-bit elements spread over the warp, transposed.
@@ -112,18 +118,18 @@ struct CodeInt8 : Code8 {
 template <typename C, int D>
 struct Shape {
   static constexpr int kRowBytes = D * C::kBytes;
-  static constexpr int kKChunks = kRowBytes / 64;                       // 16-byte pieces of a key a lane holds
-  static constexpr int kVBytes = kRowBytes >= 128 ? 16 : 8;             // bytes of a value a lane loads at once
-  static constexpr int kVChunks = kRowBytes / (8 * kVBytes);
-  static constexpr int kVElems = kVBytes / C::kBytes;
-  // keys a warp takes at once: 16 per product, more where rows are short, so that up to 8 KB
-  // of keys are on their way
+  static constexpr int kPitch = kRowBytes + 16;  // 8 rows of a matrix fall into different banks
+  // keys a warp takes at once: 16 per product, more where rows are short, so that a buffer
+  // holds 8 KB (4 KB at 64 bytes a row)
   static constexpr int kTiles = kRowBytes >= 512 ? 1 : kRowBytes >= 256 ? 2 : 4;
   static constexpr int kKeys = 16 * kTiles;
-  static constexpr int kBlock = kWarps * kKeys;                         // keys of a scheduling block
+  static constexpr int kBlock = kWarps * kKeys;  // keys of a scheduling block
   static constexpr int kMTiles = D / 16;
-  static constexpr int kQPad = C::kBytes == 2 ? 64 : 16;                // bytes: keeps 8 heads' reads apart in the banks
-  static constexpr int kBlocksPerSm = 2;
+  static constexpr int kBuf = kKeys * kPitch;    // bytes of a buffer
+  static constexpr int kRing = 3 * kBuf;
+  static constexpr int kHeadPitch = D + 4;       // floats: the warps' sums on their way to each other
+  static_assert(kHeadsPerUnit * kHeadPitch * 4 <= kRing, "a warp's sums fit its ring");
+  static constexpr int kSmem = kWarps * kRing;
 };
 
 // Work: units u = (sample, kv head, group of up to 8 query heads), each of ceil(len/kBlock)
@@ -138,9 +144,9 @@ struct Look {
 };
 template <int N>
 struct Step {
-  int rows[N];
-  unsigned seen[N];
-  bool any;
+  int rows[N];           // pool rows, -1: unseen
+  unsigned seen[N];      // a bit for each visible key
+  float ks[N], vs[N];    // 8-bit codes: scales
 };
 //
 // Split units are listed in the workspace: by unit if there are no more units than CTAs,
@@ -165,12 +171,12 @@ constexpr int kPartFloats = kHeadsPerUnit * D + 2 * kHeadsPerUnit;
 }  // namespace
 
 template <typename C, int D>
-__global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_attend(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) k_attend(const __grid_constant__ AttendArgs a) {
   using S = Shape<C, D>;
   pdl_wait();
   pdl_trigger();
-  __shared__ __align__(16) float sm_o[kWarps][kHeadsPerUnit][D];
-  __shared__ __align__(16) uint8_t sm_q[kHeadsPerUnit][D * 2 + S::kQPad];
+  extern __shared__ __align__(16) uint8_t sm_ring[];
+  __shared__ __align__(16) uint8_t sm_q[kHeadsPerUnit][D * 2 + 16];
   __shared__ float sm_m[kWarps][kHeadsPerUnit], sm_l[kWarps][kHeadsPerUnit], sm_qf[kHeadsPerUnit];
   __shared__ int sm_scan[kWarps], sm_b, sm_at;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -265,10 +271,18 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_atte
     }
     __syncthreads();
 
-    const int64_t row_bytes = (int64_t)a.kv * S::kRowBytes;
-    const uint8_t *kbase = (const uint8_t *)a.kp.codes + (int64_t)h * S::kRowBytes + t * 16;
-    const uint8_t *vbase = (const uint8_t *)a.vp.codes + (int64_t)h * S::kRowBytes + g * S::kVBytes;
     const float qf0 = sm_qf[2 * t], qf1 = sm_qf[2 * t + 1];
+    uint32_t qb[S::kMTiles][2];  // Q^T: column (head) g, in the order in which a lane's keys come
+#pragma unroll
+    for (int i = 0; i < S::kMTiles; ++i) {
+      const uint8_t *p = &sm_q[g][32 * i + (C::kScaled ? 8 : 4) * t];
+      qb[i][0] = *reinterpret_cast<const uint32_t *>(p);
+      qb[i][1] = *reinterpret_cast<const uint32_t *>(p + (C::kScaled ? 4 : 16));
+    }
+
+    const uint32_t row_bytes = (uint32_t)a.kv * S::kRowBytes;
+    const uint8_t *kbase = (const uint8_t *)a.kp.codes + (int64_t)h * S::kRowBytes;
+    const uint8_t *vbase = (const uint8_t *)a.vp.codes + (int64_t)h * S::kRowBytes;
     const int key_end = min(len, (blk0 + nseg) * S::kBlock);
     const int key_0 = blk0 * S::kBlock + warp * S::kKeys;
     constexpr int kRegs = (S::kKeys + 31) / 32;  // a lane keeps key i of a step, and key 32 + i of longer ones
@@ -279,20 +293,16 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_atte
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
     float w0 = -INFINITY, w1 = -INFINITY;  // 8-bit codes: running maximum of s + log2(value scale)
 
-    // A step's keys.  look() issues the loads of page numbers and mask two steps ahead and
-    // settle(), a step later, takes what came: seen has a bit for each visible key, and rows
-    // their pool rows.  An unseen key takes the row of a seen one of the step (its scores are
-    // dropped), so that no load has a condition and nothing but visible rows is read, whose
-    // values may stand beside weights of zero; a step without a visible key reads nothing.
+    // look() issues the loads of a step's page numbers and mask, settle(), a step later, takes
+    // what came.  Unseen keys are not read: their rows are filled with zeros.
     auto look = [&](int key) {
       Look<kRegs> k;
 #pragma unroll
       for (int r = 0; r < kRegs; ++r) {
         const int i = r * 32 + lane, p = key + i;
-        const bool in = i < S::kKeys && p < key_end;
         k.page[r] = -1;
         k.on[r] = 1;
-        if (in) {
+        if (i < S::kKeys && p < key_end) {
           k.page[r] = a.pt.table[(int64_t)b * a.pt.max_pages + (uint32_t)p / (uint32_t)a.pt.page_size];
           if (a.mask) k.on[r] = a.mask[(int64_t)b * a.mask_len + p];
         }
@@ -301,183 +311,179 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_atte
     };
     auto settle = [&](const Look<kRegs> &k, int key) {
       Step<kRegs> st;
-      int first = -1;
 #pragma unroll
       for (int r = 0; r < kRegs; ++r) {
         const bool ok = k.on[r] && k.page[r] >= 0 && k.page[r] < a.pt.num_pages;
-        st.rows[r] = k.page[r] * a.pt.page_size + (int)((uint32_t)(key + r * 32 + lane) % (uint32_t)a.pt.page_size);
+        st.rows[r] = ok ? k.page[r] * a.pt.page_size + (int)((uint32_t)(key + r * 32 + lane) % (uint32_t)a.pt.page_size) : -1;
         st.seen[r] = __ballot_sync(kFull, ok);
-        if (first < 0 && st.seen[r]) first = __shfl_sync(kFull, st.rows[r], __ffs(st.seen[r]) - 1);
+        st.ks[r] = st.vs[r] = 0.0f;
+        if constexpr (C::kScaled)
+          if (ok) {
+            st.ks[r] = a.kp.scale[(int64_t)st.rows[r] * a.kv + h];
+            st.vs[r] = a.vp.scale[(int64_t)st.rows[r] * a.kv + h];
+          }
       }
-      st.any = first >= 0;
-#pragma unroll
-      for (int r = 0; r < kRegs; ++r)
-        if (!(st.seen[r] >> lane & 1)) st.rows[r] = first;
       return st;
     };
-    uint32_t kc[S::kTiles][2][S::kKChunks][4];
-    float ks[kRegs];
-    auto load_k = [&](const Step<kRegs> &st) {
+    const uint32_t ring = smem_u32(sm_ring) + warp * S::kRing;
+    // A step's rows into a buffer: kRowBytes / 16 lanes a row, consecutive bytes.
+    auto copy = [&](const Step<kRegs> &st, const uint8_t *base, int buf) {
+      constexpr int kLanes = S::kRowBytes / 16, kAtOnce = 32 / kLanes;
+      const uint8_t *src = base + lane % kLanes * 16;
+      const uint32_t dst = ring + buf * S::kBuf + lane / kLanes * S::kPitch + lane % kLanes * 16;
 #pragma unroll
-      for (int u = 0; u < S::kTiles; ++u)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const uint8_t *p = kbase + of_key(st.rows, u, half * 8 + g) * row_bytes;
-#pragma unroll
-          for (int i = 0; i < S::kKChunks; ++i) load_codes<4>(kc[u][half][i], p + i * 64);
-        }
-      if constexpr (C::kScaled)
-#pragma unroll
-        for (int r = 0; r < kRegs; ++r) ks[r] = a.kp.scale[(int64_t)st.rows[r] * a.kv + h];
-    };
-
-    Step<kRegs> now = settle(look(key_0), key_0);
-    if (now.any) load_k(now);
-    Look<kRegs> ahead = look(key_0 + S::kBlock);
-    for (int key = key_0; key < key_end; key += S::kBlock) {
-      // values of this step: on their way while the scores are formed
-      uint32_t vc[S::kTiles][4][S::kVChunks][S::kVBytes / 4];
-      float vs[kRegs];
-      float s[S::kTiles][4];
-      if (now.any) {
-#pragma unroll
-        for (int u = 0; u < S::kTiles; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint8_t *p = vbase + of_key(now.rows, u, 2 * t + (i & 1) + (i >> 1) * 8) * row_bytes;
-#pragma unroll
-            for (int j = 0; j < S::kVChunks; ++j) load_codes<S::kVBytes / 4>(vc[u][i][j], p + j * 8 * S::kVBytes);
-          }
-        if constexpr (C::kScaled)
-#pragma unroll
-          for (int r = 0; r < kRegs; ++r) vs[r] = a.vp.scale[(int64_t)now.rows[r] * a.kv + h];
-
-        // S^T = K Q^T: rows (keys) g and g + 8, columns (heads) 2t and 2t + 1
-#pragma unroll
-        for (int u = 0; u < S::kTiles; ++u) {
-          float x[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};  // two chains
-          if constexpr (C::kScaled) {
-#pragma unroll
-            for (int i = 0; i < S::kKChunks; ++i) {
-              uint32_t qb[8];
-              const uint8_t *qp = &sm_q[g][i * 128 + t * 32];
-              *reinterpret_cast<uint4 *>(&qb[0]) = *reinterpret_cast<const uint4 *>(qp);
-              *reinterpret_cast<uint4 *>(&qb[4]) = *reinterpret_cast<const uint4 *>(qp + 16);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                uint32_t a0, a1, a2, a3;
-                C::halves(kc[u][0][i][r], a0, a2);
-                C::halves(kc[u][1][i][r], a1, a3);
-                C::mma(x[r & 1], a0, a1, a2, a3, qb[2 * r], qb[2 * r + 1]);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < S::kKChunks; ++i) {
-              uint32_t qb[4];
-              *reinterpret_cast<uint4 *>(&qb[0]) = *reinterpret_cast<const uint4 *>(&sm_q[g][i * 64 + t * 16]);
-              C::mma(x[0], kc[u][0][i][0], kc[u][1][i][0], kc[u][0][i][1], kc[u][1][i][1], qb[0], qb[1]);
-              C::mma(x[1], kc[u][0][i][2], kc[u][1][i][2], kc[u][0][i][3], kc[u][1][i][3], qb[2], qb[3]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[u][i] = (x[0][i] + x[1][i]) * ((i & 1) ? qf1 : qf0);
-          if constexpr (C::kScaled) {
-            const float ka = of_key(ks, u, g), kb = of_key(ks, u, 8 + g);
-            s[u][0] *= ka, s[u][1] *= ka, s[u][2] *= kb, s[u][3] *= kb;
-          }
-          const unsigned seen = now.seen[(u * 16) / 32] >> ((u * 16) % 32 + g);
-          if (!(seen & 1)) s[u][0] = s[u][1] = -INFINITY;
-          if (!(seen >> 8 & 1)) s[u][2] = s[u][3] = -INFINITY;
-        }
+      for (int i = 0; i < S::kKeys; i += kAtOnce) {
+        const int row = __shfl_sync(kFull, st.rows[i / 32], i % 32 + lane / kLanes);
+        cp_async16(dst + i * S::kPitch, src + (uint64_t)(uint32_t)max(row, 0) * row_bytes, row >= 0);
       }
-      const Step<kRegs> coming = settle(ahead, key + S::kBlock);
-      ahead = look(key + 2 * S::kBlock);
-      if (coming.any) load_k(coming);
-      if (now.any) {
-        // online softmax: columns are heads, so a lane's two factors serve its scores and its sums
-        float n0 = m0, n1 = m1;
+    };
+    auto next_buf = [](int buf) { return buf == 2 ? 0 : buf + 1; };
+
+    Look<kRegs> k0 = look(key_0), ahead = look(key_0 + S::kBlock);
+    Step<kRegs> now = settle(k0, key_0);
+    int kbuf = 0;
+    if (key_0 < key_end) {
+      copy(now, kbase, 0);
+      cp_async_commit();
+      copy(now, vbase, 1);
+      cp_async_commit();
+    }
+    Step<kRegs> next = settle(ahead, key_0 + S::kBlock);
+    if (key_0 + S::kBlock < key_end) copy(next, kbase, 2);
+    cp_async_commit();
+    ahead = look(key_0 + 2 * S::kBlock);
+    for (int key = key_0; key < key_end; key += S::kBlock) {
+      // committed by now: this step's K and V and the next one's K
+      cp_async_wait<2>();
+      __syncwarp();
+      // S^T = K Q^T: rows (keys) g and g + 8, columns (heads) 2t and 2t + 1
+      float s[S::kTiles][4];
+#pragma unroll
+      for (int u = 0; u < S::kTiles; ++u) {
+        float x[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};  // two chains
+        const uint32_t at_k = ring + kbuf * S::kBuf + (u * 16 + lane % 16) * S::kPitch + lane / 16 * 16;
+#pragma unroll
+        for (int i = 0; i < S::kRowBytes / 32; ++i) {
+          uint32_t r[4];
+          ldsm(r, at_k + 32 * i);
+          if constexpr (C::kScaled) {
+            uint32_t a0, a1, a2, a3;
+            C::halves(r[0], a0, a2);
+            C::halves(r[1], a1, a3);
+            C::mma(x[0], a0, a1, a2, a3, qb[2 * i][0], qb[2 * i][1]);
+            C::halves(r[2], a0, a2);
+            C::halves(r[3], a1, a3);
+            C::mma(x[1], a0, a1, a2, a3, qb[2 * i + 1][0], qb[2 * i + 1][1]);
+          } else {
+            C::mma(x[i & 1], r[0], r[1], r[2], r[3], qb[i][0], qb[i][1]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[u][i] = (x[0][i] + x[1][i]) * ((i & 1) ? qf1 : qf0);
+        if constexpr (C::kScaled) {
+          const float ka = of_key(now.ks, u, g), kb = of_key(now.ks, u, 8 + g);
+          s[u][0] *= ka, s[u][1] *= ka, s[u][2] *= kb, s[u][3] *= kb;
+        }
+        const unsigned seen = now.seen[(u * 16) / 32] >> ((u * 16) % 32 + g);
+        if (!(seen & 1)) s[u][0] = s[u][1] = -INFINITY;
+        if (!(seen >> 8 & 1)) s[u][2] = s[u][3] = -INFINITY;
+      }
+      __syncwarp();
+      if (key + S::kBlock < key_end) copy(next, vbase, kbuf);  // the next step's V takes K's buffer
+      cp_async_commit();
+      const int vbuf = next_buf(kbuf);
+
+      // online softmax: columns are heads, so a lane's two factors serve its scores and its sums
+      float n0 = m0, n1 = m1;
+#pragma unroll
+      for (int u = 0; u < S::kTiles; ++u) {
+        n0 = fmaxf(n0, fmaxf(s[u][0], s[u][2]));
+        n1 = fmaxf(n1, fmaxf(s[u][1], s[u][3]));
+      }
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, d));
+        n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, d));
+      }
+      const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
+      float f0 = ex2_approx(m0 - z0), f1 = ex2_approx(m1 - z1);
+      l0 *= f0, l1 *= f1;
+      m0 = n0, m1 = n1;
+      float p[S::kTiles][4];
+#pragma unroll
+      for (int u = 0; u < S::kTiles; ++u) {
+        p[u][0] = ex2_approx(s[u][0] - z0), p[u][2] = ex2_approx(s[u][2] - z0);
+        p[u][1] = ex2_approx(s[u][1] - z1), p[u][3] = ex2_approx(s[u][3] - z1);
+        l0 += p[u][0] + p[u][2];
+        l1 += p[u][1] + p[u][3];
+      }
+      if constexpr (C::kScaled) {
+        // A value's scale goes into its weight: 2^(s + log2 scale - w) with a maximum w of its
+        // own, which keeps the fp16 weights in range whatever the scales are.
+        float e0 = w0, e1 = w1, lv[kRegs];
+#pragma unroll
+        for (int r = 0; r < kRegs; ++r) lv[r] = log2_approx(now.vs[r]);
 #pragma unroll
         for (int u = 0; u < S::kTiles; ++u) {
-          n0 = fmaxf(n0, fmaxf(s[u][0], s[u][2]));
-          n1 = fmaxf(n1, fmaxf(s[u][1], s[u][3]));
+          const float va = of_key(lv, u, g), vb = of_key(lv, u, 8 + g);
+          s[u][0] += va, s[u][1] += va, s[u][2] += vb, s[u][3] += vb;
+          e0 = fmaxf(e0, fmaxf(s[u][0], s[u][2]));
+          e1 = fmaxf(e1, fmaxf(s[u][1], s[u][3]));
         }
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
-          n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, d));
-          n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, d));
+          e0 = fmaxf(e0, __shfl_xor_sync(kFull, e0, d));
+          e1 = fmaxf(e1, __shfl_xor_sync(kFull, e1, d));
         }
-        const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
-        float f0 = ex2_approx(m0 - z0), f1 = ex2_approx(m1 - z1);
-        l0 *= f0, l1 *= f1;
-        m0 = n0, m1 = n1;
-        float p[S::kTiles][4];
+        const float y0 = e0 == -INFINITY ? 0.0f : e0, y1 = e1 == -INFINITY ? 0.0f : e1;
+        f0 = ex2_approx(w0 - y0), f1 = ex2_approx(w1 - y1);
+        w0 = e0, w1 = e1;
 #pragma unroll
         for (int u = 0; u < S::kTiles; ++u) {
-          p[u][0] = ex2_approx(s[u][0] - z0), p[u][2] = ex2_approx(s[u][2] - z0);
-          p[u][1] = ex2_approx(s[u][1] - z1), p[u][3] = ex2_approx(s[u][3] - z1);
-          l0 += p[u][0] + p[u][2];
-          l1 += p[u][1] + p[u][3];
-        }
-        if constexpr (C::kScaled) {
-          // A value's scale goes into its weight: 2^(s + log2 scale - w) with a maximum w of its
-          // own, which keeps the fp16 weights in range whatever the scales are.
-          float e0 = w0, e1 = w1;
-#pragma unroll
-          for (int r = 0; r < kRegs; ++r) vs[r] = log2_approx(vs[r]);
-#pragma unroll
-          for (int u = 0; u < S::kTiles; ++u) {
-            const float va = of_key(vs, u, g), vb = of_key(vs, u, 8 + g);
-            s[u][0] += va, s[u][1] += va, s[u][2] += vb, s[u][3] += vb;
-            e0 = fmaxf(e0, fmaxf(s[u][0], s[u][2]));
-            e1 = fmaxf(e1, fmaxf(s[u][1], s[u][3]));
-          }
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) {
-            e0 = fmaxf(e0, __shfl_xor_sync(kFull, e0, d));
-            e1 = fmaxf(e1, __shfl_xor_sync(kFull, e1, d));
-          }
-          const float y0 = e0 == -INFINITY ? 0.0f : e0, y1 = e1 == -INFINITY ? 0.0f : e1;
-          f0 = ex2_approx(w0 - y0), f1 = ex2_approx(w1 - y1);
-          w0 = e0, w1 = e1;
-#pragma unroll
-          for (int u = 0; u < S::kTiles; ++u) {
-            p[u][0] = ex2_approx(s[u][0] - y0), p[u][2] = ex2_approx(s[u][2] - y0);
-            p[u][1] = ex2_approx(s[u][1] - y1), p[u][3] = ex2_approx(s[u][3] - y1);
-          }
-        }
-        if (__any_sync(kFull, !(f0 == 1.0f && f1 == 1.0f))) {
-#pragma unroll
-          for (int i = 0; i < S::kMTiles; ++i) o[i][0] *= f0, o[i][1] *= f1, o[i][2] *= f0, o[i][3] *= f1;
-        }
-
-        // O^T += V^T P^T: the scores' layout, transposed 8 x 8, is the operand's
-#pragma unroll
-        for (int u = 0; u < S::kTiles; ++u) {
-          const uint32_t b0 = transpose8x8(C::pack(p[u][0], p[u][1]));
-          const uint32_t b1 = transpose8x8(C::pack(p[u][2], p[u][3]));
-#pragma unroll
-          for (int j = 0; j < S::kVChunks; ++j)
-#pragma unroll
-            for (int x = 0; x < S::kVBytes / 4; ++x) {
-              const uint32_t v0 = vc[u][0][j][x], v1 = vc[u][1][j][x], v2 = vc[u][2][j][x], v3 = vc[u][3][j][x];
-              if constexpr (C::kScaled) {
-                uint32_t a0, a1, a2, a3;
-                const int mt = j * (S::kVElems / 2) + 2 * x;
-                C::halves(prmt(v0, v1, 0x5140), a0, a1);
-                C::halves(prmt(v2, v3, 0x5140), a2, a3);
-                C::mma(o[mt], a0, a1, a2, a3, b0, b1);
-                C::halves(prmt(v0, v1, 0x7362), a0, a1);
-                C::halves(prmt(v2, v3, 0x7362), a2, a3);
-                C::mma(o[mt + 1], a0, a1, a2, a3, b0, b1);
-              } else {
-                C::mma(o[j * (S::kVElems / 2) + x], prmt(v0, v1, 0x5410), prmt(v0, v1, 0x7632), prmt(v2, v3, 0x5410),
-                       prmt(v2, v3, 0x7632), b0, b1);
-              }
-            }
+          p[u][0] = ex2_approx(s[u][0] - y0), p[u][2] = ex2_approx(s[u][2] - y0);
+          p[u][1] = ex2_approx(s[u][1] - y1), p[u][3] = ex2_approx(s[u][3] - y1);
         }
       }
-      now = coming;
+      if (__any_sync(kFull, !(f0 == 1.0f && f1 == 1.0f))) {
+#pragma unroll
+        for (int i = 0; i < S::kMTiles; ++i) o[i][0] *= f0, o[i][1] *= f1, o[i][2] *= f0, o[i][3] *= f1;
+      }
+
+      // O^T += V^T P^T: rows are dims (16i + g and 16i + 8 + g in bf16, 16i + 2g and + 1 of 8-bit codes)
+      cp_async_wait<2>();
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < S::kTiles; ++u) {
+        const uint32_t b0 = transpose8x8(C::pack(p[u][0], p[u][1]));
+        const uint32_t b1 = transpose8x8(C::pack(p[u][2], p[u][3]));
+        const int half = lane / 16, odd = lane / 8 % 2;  // bf16: keys, dims; 8-bit codes: dims, keys
+        const uint32_t at_v = ring + vbuf * S::kBuf + (u * 16 + (C::kScaled ? odd : half) * 8 + lane % 8) * S::kPitch +
+                              (C::kScaled ? half : odd) * 16;
+#pragma unroll
+        for (int i = 0; i < S::kRowBytes / 32; ++i) {
+          uint32_t r[4];
+          ldsm_t(r, at_v + 32 * i);
+          if constexpr (C::kScaled) {
+            // a word: (dim 2g, 2g + 1) of key 2t, then of key 2t + 1
+            uint32_t a0, a1, a2, a3;
+            C::halves(prmt(r[0], 0, 0x3120), a0, a1);
+            C::halves(prmt(r[1], 0, 0x3120), a2, a3);
+            C::mma(o[2 * i], a0, a1, a2, a3, b0, b1);
+            C::halves(prmt(r[2], 0, 0x3120), a0, a1);
+            C::halves(prmt(r[3], 0, 0x3120), a2, a3);
+            C::mma(o[2 * i + 1], a0, a1, a2, a3, b0, b1);
+          } else {
+            C::mma(o[i], r[0], r[1], r[2], r[3], b0, b1);
+          }
+        }
+      }
+      __syncwarp();
+      now = next;
+      next = settle(ahead, key + 2 * S::kBlock);
+      if (key + 2 * S::kBlock < key_end) copy(next, kbase, vbuf);  // the K after the next takes V's buffer
+      cp_async_commit();
+      ahead = look(key + 3 * S::kBlock);
+      kbuf = next_buf(vbuf);
     }
 
     // ---- the warps' sums together
@@ -496,11 +502,19 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_atte
       sm_m[warp][2 * t] = m0, sm_m[warp][2 * t + 1] = m1;
       sm_l[warp][2 * t] = l0, sm_l[warp][2 * t + 1] = l1;
     }
+    cp_async_wait<0>();  // the ring is empty: its first bytes take this warp's sums
+    __syncwarp();
+    float *mine_o = reinterpret_cast<float *>(sm_ring + warp * S::kRing);
 #pragma unroll
     for (int i = 0; i < S::kMTiles; ++i) {
-      const int d = i / (S::kVElems / 2) * 8 * S::kVElems + g * S::kVElems + i % (S::kVElems / 2) * 2;
-      *reinterpret_cast<float2 *>(&sm_o[warp][2 * t][d]) = make_float2(o[i][0], o[i][2]);
-      *reinterpret_cast<float2 *>(&sm_o[warp][2 * t + 1][d]) = make_float2(o[i][1], o[i][3]);
+      float *p0 = mine_o + 2 * t * S::kHeadPitch + 16 * i + (C::kScaled ? 2 : 1) * g, *p1 = p0 + S::kHeadPitch;
+      if constexpr (C::kScaled) {
+        *reinterpret_cast<float2 *>(p0) = make_float2(o[i][0], o[i][2]);
+        *reinterpret_cast<float2 *>(p1) = make_float2(o[i][1], o[i][3]);
+      } else {
+        p0[0] = o[i][0], p0[8] = o[i][2];
+        p1[0] = o[i][1], p1[8] = o[i][3];
+      }
     }
     __syncthreads();
     const bool whole = nseg == nblk;
@@ -516,7 +530,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_atte
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = sm_m[w][n] == -INFINITY ? 0.0f : ex2_approx(sm_m[w][n] - mm);
-        const float4 y = *reinterpret_cast<const float4 *>(&sm_o[w][n][d]);
+        const float4 y = *reinterpret_cast<const float4 *>(sm_ring + w * S::kRing + (n * S::kHeadPitch + d) * 4);
         x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
         l += f * sm_l[w][n];
       }
@@ -548,13 +562,17 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm) k_atte
 // Adds up the parts of split unit blockIdx.x, in order of the keys.  A part is 8 heads x D/4
 // vectors; blockIdx.y takes an equal share of them, so that a few units with hundreds of
 // parts spread over many SMs.  Threads beyond a share's vectors take turns at the parts.
+// Bound by the L2's latency: the first parts are loaded while the weights are formed, the
+// others kAhead at a time.
 template <int D>
-__global__ void __launch_bounds__(256) k_attend_join(const __grid_constant__ AttendArgs a, int grid) {
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_constant__ AttendArgs a, int grid) {
   pdl_wait();
   pdl_trigger();
-  constexpr int kChunk = 32, kAhead = 4, kStats = kHeadsPerUnit * D;
-  __shared__ float sm_w[kChunk][kHeadsPerUnit], sm_max[8][kHeadsPerUnit], sm_sum[8][kHeadsPerUnit];
-  __shared__ float4 sm_x[256];
+  constexpr int kAhead = 8, kStats = kHeadsPerUnit * D, kJoinWarps = kJoinThreads / 32;
+  constexpr int kAtOnce = kJoinThreads / kHeadsPerUnit;  // parts whose statistics are read at once
+  __shared__ float sm_w[kMaxGrid][kHeadsPerUnit], sm_l[kMaxGrid][kHeadsPerUnit];
+  __shared__ float sm_red[kJoinWarps][kHeadsPerUnit];
+  __shared__ float4 sm_x[kJoinThreads];
   const Split sp = reinterpret_cast<const Split *>(a.part)[blockIdx.x];
   if (sp.unit < 0) return;
   const float *parts = a.part + grid * (sizeof(Split) / 4);
@@ -565,77 +583,72 @@ __global__ void __launch_bounds__(256) k_attend_join(const __grid_constant__ Att
   const int count = sp.last - sp.first + 1;
   auto part_of = [&](int i) { return parts + (int64_t)(i == 0 ? sp.slot : 2 * (sp.first + i)) * kPartFloats<D>; };
 
-  const int share = 2 * D / gridDim.y, lanes = min(share, 256), turns = 256 / lanes, turn = tid / lanes;
-  const int n = tid & 7, i_of = tid >> 3;  // this thread's head and part of a chunk's statistics
-  for (int v0 = 0; v0 < share; v0 += lanes) {
-    const int v = blockIdx.y * share + v0 + tid % lanes, head = v / (D / 4);
-    const bool mine = head < nh;
-    float4 ahead[kAhead];  // on their way while the weights are formed
+  const int lanes = 2 * D / gridDim.y, turns = kJoinThreads / lanes, turn = tid / lanes;  // lanes <= kJoinThreads
+  const int v = blockIdx.y * lanes + tid % lanes, head = v / (D / 4);
+  const bool mine = head < nh;
+  float4 ahead[kAhead];
+  auto load = [&](int j0) {
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) {
-      const int j = turn + q * turns;
+      const int j = j0 + q * turns;
       ahead[q] = make_float4(0, 0, 0, 0);
-      if (mine && j < min(count, kChunk)) ahead[q] = *reinterpret_cast<const float4 *>(part_of(j) + 4 * v);
+      if (mine && j < count) ahead[q] = *reinterpret_cast<const float4 *>(part_of(j) + 4 * v);
     }
-    float mm = -INFINITY;
-    if (n < nh)
-      for (int i = i_of; i < count; i += kChunk) mm = fmaxf(mm, part_of(i)[kStats + 2 * n]);
-    mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, 8));
-    mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, 16));
-    if (lane < 8) sm_max[warp][n] = mm;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 8; ++w) mm = fmaxf(mm, sm_max[w][n]);
+  };
+  load(turn);
 
-    float l = 0.0f;
-    float4 x = make_float4(0, 0, 0, 0);
-    auto add = [&](float f, const float4 &y) { x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w; };
-    for (int i0 = 0; i0 < count; i0 += kChunk) {
-      const int i = i0 + i_of;
-      float w = 0.0f;
-      if (n < nh && i < count) {
-        const float m = part_of(i)[kStats + 2 * n];
-        w = m == -INFINITY ? 0.0f : ex2_approx(m - mm);
-        l += w * part_of(i)[kStats + 2 * n + 1];
-      }
-      sm_w[i_of][n] = w;
-      __syncthreads();
-      const int here = min(kChunk, count - i0);
-      int j = turn;
-      if (i0 == 0) {
-#pragma unroll
-        for (int q = 0; q < kAhead; ++q, j += turns)
-          if (j < here) add(sm_w[j][head], ahead[q]);
-      }
-      if (mine)
+  // weights of the parts, and the sum of their l
+  const int n = tid % kHeadsPerUnit;
+  float mm = -INFINITY;
+  if (n < nh)
 #pragma unroll 4
-        for (; j < here; j += turns) add(sm_w[j][head], *reinterpret_cast<const float4 *>(part_of(i0 + j) + 4 * v));
-      __syncthreads();
+    for (int i = tid / kHeadsPerUnit; i < count; i += kAtOnce) {
+      const float2 ml = *reinterpret_cast<const float2 *>(part_of(i) + kStats + 2 * n);
+      sm_w[i][n] = ml.x;
+      sm_l[i][n] = ml.y;
+      mm = fmaxf(mm, ml.x);
     }
-    l += __shfl_xor_sync(kFull, l, 8);
-    l += __shfl_xor_sync(kFull, l, 16);
-    if (lane < 8) sm_sum[warp][n] = l;
-    sm_x[tid] = x;
-    __syncthreads();
-    if (tid < lanes && mine) {
-      l = 0.0f;
+  mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, 8));
+  mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, 16));
+  if (lane < 8) sm_red[warp][n] = mm;
+  __syncthreads();
 #pragma unroll
-      for (int w = 0; w < 8; ++w) l += sm_sum[w][head];
-      for (int j = 1; j < turns; ++j) add(1.0f, sm_x[j * lanes + tid]);
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const int64_t at = (int64_t)b * a.heads + h0 + head;
-      const int d = v % (D / 4) * 4;
-      *reinterpret_cast<uint2 *>(a.out + at * D + d) =
-          make_uint2(CodeBf16::pack(x.x * inv, x.y * inv), CodeBf16::pack(x.z * inv, x.w * inv));
-      if (d == 0 && a.lse) {
-        mm = sm_max[0][head];
-#pragma unroll
-        for (int w = 1; w < 8; ++w) mm = fmaxf(mm, sm_max[w][head]);
-        a.lse[at] = l == 0.0f ? -INFINITY : (mm + log2f(l)) * 0.6931471805599453f;
-      }
+  for (int w = 0; w < kJoinWarps; ++w) mm = fmaxf(mm, sm_red[w][n]);
+  __syncthreads();
+  float l = 0.0f;
+  if (n < nh)
+    for (int i = tid / kHeadsPerUnit; i < count; i += kAtOnce) {
+      const float m = sm_w[i][n], w = m == -INFINITY ? 0.0f : ex2_approx(m - mm);
+      sm_w[i][n] = w;
+      l += w * sm_l[i][n];
     }
-    __syncthreads();
+  l += __shfl_xor_sync(kFull, l, 8);
+  l += __shfl_xor_sync(kFull, l, 16);
+  if (lane < 8) sm_red[warp][n] = l;
+  if (tid < kHeadsPerUnit) sm_l[0][n] = mm;  // only this thread read it
+  __syncthreads();
+
+  float4 x = make_float4(0, 0, 0, 0);
+  auto add = [&](float f, const float4 &y) { x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w; };
+  for (int j0 = turn; mine && j0 < count; j0 += kAhead * turns) {
+    if (j0 != turn) load(j0);
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+      if (j0 + q * turns < count) add(sm_w[j0 + q * turns][head], ahead[q]);
   }
+  sm_x[tid] = x;
+  __syncthreads();
+  if (tid >= lanes || !mine) return;
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) l += sm_red[w][head];
+  for (int j = 1; j < turns; ++j) add(1.0f, sm_x[j * lanes + tid]);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const int64_t at = (int64_t)b * a.heads + h0 + head;
+  const int d = v % (D / 4) * 4;
+  *reinterpret_cast<uint2 *>(a.out + at * D + d) =
+      make_uint2(CodeBf16::pack(x.x * inv, x.y * inv), CodeBf16::pack(x.z * inv, x.w * inv));
+  if (d == 0 && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (sm_l[0][head] + log2f(l)) * 0.6931471805599453f;
 }
 
 namespace {
@@ -646,8 +659,7 @@ int attend_grid(int B, int heads, int kv, int page_size, int max_pages) {
   using S = Shape<C, D>;
   const int64_t cap = (int64_t)page_size * max_pages;
   const int64_t most = (int64_t)B * kv * head_groups(heads, kv) * ((cap + S::kBlock - 1) / S::kBlock);
-  const int64_t resident = (int64_t)148 * S::kBlocksPerSm;
-  return (int)(most < resident ? most : resident);
+  return (int)(most < kMaxGrid ? most : kMaxGrid);
 }
 template <typename C, int D>
 size_t attend_bytes(int B, int heads, int kv, int page_size, int max_pages) {
@@ -657,13 +669,15 @@ size_t attend_bytes(int B, int heads, int kv, int page_size, int max_pages) {
 template <typename C, int D>
 cudaError_t attend_go(const AttendArgs &a, cudaStream_t s) {
   const int grid = attend_grid<C, D>(a.B, a.heads, a.kv, a.pt.page_size, a.pt.max_pages);
-  const cudaError_t e = launch_pdl(k_attend<C, D>, dim3(grid), kWarps * 32, 0, s, a);
+  using S = Shape<C, D>;
+  cudaError_t e = cudaFuncSetAttribute(k_attend<C, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e == cudaSuccess) e = launch_pdl(k_attend<C, D>, dim3(grid), kWarps * 32, S::kSmem, s, a);
   if (e != cudaSuccess || grid == 1) return e;  // one CTA: nothing is split
   const int64_t units = (int64_t)a.B * a.kv * head_groups(a.heads, a.kv);
   const int lists = (int)(units < grid ? units : grid);
   int shares = 1;  // about one CTA an SM in all, 16 vectors or more each
   while (shares < D / 8 && lists * shares < 148) shares *= 2;
-  return launch_pdl(k_attend_join<D>, dim3(lists, shares), 256, 0, s, a, grid);
+  return launch_pdl(k_attend_join<D>, dim3(lists, shares), kJoinThreads, 0, s, a, grid);
 }
 
 #define PI0X_PICK(fn, dtype, dim, ...)                                                                      \
