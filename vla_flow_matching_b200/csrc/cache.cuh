@@ -25,22 +25,37 @@ struct PoolPtr {
   float *scale;
 };
 
+// n / d for 0 <= n < 2^31 by a product: q = (hi32(n * m) + n) >> l with l = ceil(log2 d) and
+// m = floor(2^32 (2^l - d) / d) + 1 (Granlund and Montgomery, 1994).
+struct FastDiv {
+  uint32_t d, m, l;
+  FastDiv() = default;
+  __host__ explicit FastDiv(uint32_t div) : d(div), l(0) {
+    while ((1ull << l) < div) ++l;
+    m = (uint32_t)(((1ull << 32) * ((1ull << l) - div)) / div + 1);
+  }
+  __host__ __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    return (uint32_t)((((uint64_t)n * m >> 32) + n) >> l);
+  }
+};
+
 struct PageTable {
   const int *table;   // (B, max_pages)
   int max_pages, page_size, num_pages;
+  FastDiv by_page;    // by page_size
 };
 
 // Row of the pool that holds slot `pos` of sample b, or -1 (no page there).
 __host__ __device__ __forceinline__ int cache_row(const PageTable &pt, int b, int64_t pos) {
   if (pos < 0 || pos >= (int64_t)pt.max_pages * pt.page_size) return -1;
-  const uint32_t at = (uint32_t)pos / (uint32_t)pt.page_size, off = (uint32_t)pos - at * (uint32_t)pt.page_size;
+  const uint32_t at = pt.by_page.div((uint32_t)pos), off = (uint32_t)pos - at * (uint32_t)pt.page_size;
   const int page = pt.table[(int64_t)b * pt.max_pages + at];
   return page >= 0 && page < pt.num_pages ? page * pt.page_size + (int)off : -1;
 }
 
 // ---- norm, rotation and page writes (k_cache.cu) ---------------------------------
 struct RowArgs {
-  int B, T, hq, hk, hv;        // rows of a token: q heads, then k heads, then v heads
+  int B, T, hq, hk;            // heads of q, of k and v
   RowsPtr q, k, v, q_out, k_out;
   const int *start, *count, *positions;
   const float *q_gain, *k_gain;
@@ -48,7 +63,9 @@ struct RowArgs {
   int rotate, to_cache;
   PoolPtr kp, vp;              // to_cache: the layer's pools
   PageTable pt;
-  int per;                     // consecutive rows of a token one lane group works through
+  int per;                     // heads of a token that one lane group rotates
+  uint32_t q_blocks;           // blocks of q rows, before those of k (and v) rows
+  FastDiv by_q, by_k, by_t;    // by a token's items of q and of k, by T
   uint64_t turn[128];          // pair i turns by pos * turn[i] * 2^-64 of a full turn
 };
 cudaError_t launch_rows(const RowArgs &a, int dtype, int pool_dtype, int head_dim, cudaStream_t s);
@@ -62,6 +79,7 @@ struct ReadArgs {
   const uint8_t *mask;
   void *k_out, *v_out;
   uint8_t *mask_out;
+  FastDiv by_p, by_kv, by_b;
 };
 cudaError_t launch_cache_read(const ReadArgs &a, int dtype, int pool_dtype, int head_dim, cudaStream_t s);
 

@@ -93,7 +93,7 @@ PoolPtr layer_pool(const pi0x_cache *c, int layer, bool v) {
   return PoolPtr{codes, c->dtype == PI0X_DTYPE_BF16 ? nullptr : (v ? c->v_scale : c->k_scale) + cells};
 }
 PageTable page_table(const pi0x_cache *c, const int32_t *table, int max_pages) {
-  return PageTable{table, max_pages, c->page_size, c->num_pages};
+  return PageTable{table, max_pages, c->page_size, c->num_pages, FastDiv(c->page_size)};
 }
 
 }  // namespace pi0x
@@ -150,7 +150,7 @@ int pi0x_cache_write(const pi0x_cache *cache, int layer, int dtype, int B, int T
   a.B = B;
   a.T = T;
   a.hq = q_heads;
-  a.hk = a.hv = cache->kv_heads;
+  a.hk = cache->kv_heads;
   if (q_heads) a.q = rows_of(q), a.q_out = rows_of(q_out);
   a.k = rows_of(k);
   a.v = rows_of(v);

@@ -17,24 +17,67 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126
 
-__device__ __forceinline__ void load4(const float *p, float (&v)[4]) {
-  const float4 x = *reinterpret_cast<const float4 *>(p);
-  v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-}
-__device__ __forceinline__ void load4(const bf16 *p, float (&v)[4]) {
-  const uint2 x = *reinterpret_cast<const uint2 *>(p);
-  v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xffff0000u);
-  v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xffff0000u);
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&x);
 }
-__device__ __forceinline__ void store4(float *p, const float (&v)[4]) {
-  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+// Two fp32 values in a 64-bit register pair: sm_100 multiplies and adds both in one instruction.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
 }
-__device__ __forceinline__ void store4(bf16 *p, const float (&v)[4]) {
-  *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+__device__ __forceinline__ void split(f32x2 a, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a)); }
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// 16 bytes of a row: 8 bf16 or 4 fp32 values, in pairs.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<bf16> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ void get(const uint4 &w, f32x2 (&v)[4]) {
+    const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pair(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint4 put(const float *v) {
+    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  }
+};
+template <>
+struct Vec<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ void get(const uint4 &w, f32x2 (&v)[2]) {
+    v[0] = pair(__uint_as_float(w.x), __uint_as_float(w.y));
+    v[1] = pair(__uint_as_float(w.z), __uint_as_float(w.w));
+  }
+  static __device__ __forceinline__ uint4 put(const float *v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+// N = 4 or 8 values as bf16.
+template <int N>
+__device__ __forceinline__ void store_bf16(bf16 *p, const float (&v)[N]) {
+  if constexpr (N == 8)
+    *reinterpret_cast<uint4 *>(p) = Vec<bf16>::put(v);
+  else
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 
 // Pool element types: bf16 rows as they are, or codes of a scaled row.
@@ -50,13 +93,13 @@ struct PoolE4m3 {
     const int e = (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u);
     return __uint_as_float((uint32_t)max(e, 1) << 23);
   }
-  static __device__ __forceinline__ uint32_t codes(const float (&v)[4], float scale) {
+  static __device__ __forceinline__ uint32_t codes(const float *v, float scale) {
     const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // exact: 2^-n of 2^n
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv), __NV_SATFINITE, __NV_E4M3);
     return lo | hi << 16;
   }
-  static __device__ __forceinline__ void values(uint32_t w, float (&v)[4]) {
+  static __device__ __forceinline__ void values(uint32_t w, float *v) {
     const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
     const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
     const float2 x = __half22float2(a), y = __half22float2(b);
@@ -68,18 +111,22 @@ struct PoolInt8 {
   static __device__ __forceinline__ float scale(uint32_t top) {
     return fmaxf(__fdiv_rn(__uint_as_float(top), 127.0f), kMinScale);
   }
-  // A division per element, not a product with 1/scale: the code is then the nearest
-  // one, with nothing rounded before the last step.
-  static __device__ __forceinline__ uint32_t codes(const float (&v)[4], float scale) {
-    uint32_t w = 0;
+  // x / scale, correctly rounded before the last step, so that a code is the nearest one: with
+  // the rounded reciprocal r, q = x r and then q + (x - q scale) r is the rounded quotient
+  // (Markstein, 1990) as long as the residual is exact, which scales of 2^-100 and more
+  // guarantee.  |x / scale| is at most 127 and a rounding, so the code needs no clamp.
+  static __device__ __forceinline__ uint32_t codes(const float *v, float scale) {
+    const float r = __frcp_rn(scale);
+    int c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int c = max(-127, min(127, __float2int_rn(__fdiv_rn(v[i], scale))));
-      w |= ((uint32_t)c & 0xffu) << (8 * i);
+      float q = v[i] * r;
+      q = scale >= 7.8886091e-31f ? fmaf(fmaf(-q, scale, v[i]), r, q) : __fdiv_rn(v[i], scale);
+      c[i] = __float2int_rn(q);
     }
-    return w;
+    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
   }
-  static __device__ __forceinline__ void values(uint32_t w, float (&v)[4]) {
+  static __device__ __forceinline__ void values(uint32_t w, float *v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = (float)((int)(w << (24 - 8 * i)) >> 24);
   }
@@ -100,155 +147,288 @@ __device__ __forceinline__ void turn_cos_sin(uint32_t turn, float &c, float &s) 
   s = (quarter & 2) ? -b : b;
 }
 
+// The same to 2^-20 or so with sin.approx and cos.approx, for rows that are rounded to bf16
+// (2^-9) on their way in or out: a third of the instructions.
+__device__ __forceinline__ void turn_cos_sin_approx(uint32_t turn, float &c, float &s) {
+  const float y = (float)(int)turn * 1.4629180792671596e-9f;  // 2 pi 2^-32: [-pi, pi]
+  c = __cosf(y);
+  s = __sinf(y);
+}
+
 }  // namespace
 
-// A group of D/8 lanes holds a row: lane l the pairs (i, i + D/2), i = 4l..4l+3, so
-// that the rotation needs no exchange and loads are 8 (bf16) or 16 (fp32) bytes a lane,
-// consecutive over the group.  A group takes `per` rows of one token and forms the
-// token's cosines and sines once for them.
-template <typename T, typename Pool, int D>
-__global__ void __launch_bounds__(256) k_rows(const __grid_constant__ RowArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  constexpr int kLanes = D / 8;
-  const int rows = a.hq + a.hk + a.hv;
-  const int chunks = (rows + a.per - 1) / a.per;
-  const int64_t items = (int64_t)a.B * a.T * chunks;
-  const int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / kLanes;
-  const int l4 = (threadIdx.x % kLanes) * 4;
-  const bool live = item < items;
-  const int64_t tok = live ? item / chunks : 0;
-  const int row0 = live ? (int)(item - tok * chunks) * a.per : 0;
-  const int row1 = live ? min(rows, row0 + a.per) : 0;
-  const int b = (int)(tok / a.T), t = (int)(tok - (int64_t)b * a.T);
-  const int64_t slot = (int64_t)(a.start ? a.start[b] : 0) + t;
+// A lane holds 16 bytes of each half of a row, the pairs (i, i + D/2), so the rotation needs
+// no exchange; D/16 (bf16) or D/8 (fp32) lanes hold a row.  RowMath has what is done to a row.
+template <typename T, int D>
+struct RowMath {
+  static constexpr int kN = Vec<T>::kN, kP = kN / 2, kLanes = D / 2 / kN;
+  f32x2 c[kP], s[kP];  // cosines and sines of the lane's pairs
 
-  int cell = -1;  // row of the pools
-  if (a.to_cache && live && row1 > a.hq && (!a.count || t < a.count[b])) cell = cache_row(a.pt, b, slot);
-
-  float c[4], s[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = 1.0f, s[i] = 0.0f;
-  if (a.rotate && row0 < a.hq + a.hk) {
-    const uint64_t pos = (uint64_t)(a.positions ? (int64_t)a.positions[tok] : slot);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) turn_cos_sin((uint32_t)((pos * a.turn[l4 + i] + 0x80000000u) >> 32), c[i], s[i]);
+  // The tables in shared memory are laid out so that the lanes of a group read consecutive
+  // words: entry i of lane l is turn i * kLanes + l; gains go four at a time.
+  static __device__ __forceinline__ int turn_at(int p) { return p % kN * kLanes + p / kN; }
+  static __device__ __forceinline__ int gain_at(int d) {
+    const int p = d % (D / 2);
+    return d / (D / 2) * (D / 2) + (p % kN / 4 * kLanes + p / kN) * 4 + p % 4;
   }
 
-  for (int r = 0; r < a.per; ++r) {
-    const int row = row0 + r;
-    const bool is_q = row < a.hq, is_k = !is_q && row < a.hq + a.hk;
-    const bool put = row < row1 && (is_q || !a.to_cache || cell >= 0);
-    const int h = is_q ? row : is_k ? row - a.hq : row - a.hq - a.hk;
-    float x[4] = {0, 0, 0, 0}, y[4] = {0, 0, 0, 0};
-    if (put) {
-      const RowsPtr &src = is_q ? a.q : is_k ? a.k : a.v;
-      const T *p = (const T *)src.data + b * src.sb + t * src.st + h * src.sh + l4;
-      load4(p, x);
-      load4(p + D / 2, y);
+  // table: the lane's first entry
+  __device__ __forceinline__ void turn(int64_t pos, const uint64_t *table) {
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      float cs[2], sn[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t t = (uint32_t)(((uint64_t)pos * table[(2 * i + k) * kLanes] + 0x80000000u) >> 32);
+        if constexpr (sizeof(T) == 2)
+          turn_cos_sin_approx(t, cs[k], sn[k]);
+        else
+          turn_cos_sin(t, cs[k], sn[k]);
+      }
+      c[i] = pair(cs[0], cs[1]);
+      s[i] = pair(sn[0], sn[1]);
     }
-    const float *gain = is_q ? a.q_gain : is_k ? a.k_gain : nullptr;
-    if (a.q_gain || a.k_gain) {  // the same for every lane: the sums below are warp-wide
-      float ss = 0.0f;
+  }
+  __device__ __forceinline__ void rotate(f32x2 (&x)[kP], f32x2 (&y)[kP]) const {
+    const f32x2 minus = pair(-1.0f, -1.0f);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) ss += x[i] * x[i] + y[i] * y[i];
+    for (int i = 0; i < kP; ++i) {
+      const f32x2 v = fma2(mul2(y[i], s[i]), minus, mul2(x[i], c[i]));
+      y[i] = fma2(y[i], c[i], mul2(x[i], s[i]));
+      x[i] = v;
+    }
+  }
+  // gain: the lane's first 1 + g of the first half; the second half's are D/2 further
+  static __device__ __forceinline__ void norm(f32x2 (&x)[kP], f32x2 (&y)[kP], const float *gain, float eps) {
+    f32x2 sum = mul2(x[0], x[0]);
 #pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-      if (gain) {
-        const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
-        float g[4], g2[4];
-        load4(gain + l4, g);
-        load4(gain + D / 2 + l4, g2);
+    for (int i = 1; i < kP; ++i) sum = fma2(x[i], x[i], sum);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] = x[i] * inv * (1.0f + g[i]);
-          y[i] = y[i] * inv * (1.0f + g2[i]);
+    for (int i = 0; i < kP; ++i) sum = fma2(y[i], y[i], sum);
+    float ss, s1;
+    split(sum, ss, s1);
+    ss += s1;
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+    const float inv = rsqrtf(ss * (1.0f / D) + eps);
+    const f32x2 inv2 = pair(inv, inv);
+#pragma unroll
+    for (int i = 0; i < kP / 2; ++i) {
+      const ulonglong2 g = *reinterpret_cast<const ulonglong2 *>(gain + 4 * kLanes * i);
+      const ulonglong2 g2 = *reinterpret_cast<const ulonglong2 *>(gain + D / 2 + 4 * kLanes * i);
+      x[2 * i] = mul2(x[2 * i], mul2(inv2, g.x));
+      x[2 * i + 1] = mul2(x[2 * i + 1], mul2(inv2, g.y));
+      y[2 * i] = mul2(y[2 * i], mul2(inv2, g2.x));
+      y[2 * i + 1] = mul2(y[2 * i + 1], mul2(inv2, g2.y));
+    }
+  }
+  static __device__ __forceinline__ void floats(const f32x2 (&x)[kP], float (&u)[kN]) {
+#pragma unroll
+    for (int i = 0; i < kP; ++i) split(x[i], u[2 * i], u[2 * i + 1]);
+  }
+};
+
+// Three kinds of blocks, in this order: blocks of q rows, of k rows (rotated into k_out), or,
+// with a cache, of k and v rows on their way into pages.  An item of the first two is `per`
+// heads of one token: a group of lanes forms the token's cosines and sines once for them and
+// keeps the next kAhead rows on their way; an item of the third is one head's key and value.
+// One item a group, so that the rows are on their way before anything else is read, and
+// blocks of padding (tokens beyond a sample's count) end at once.  Bound by HBM at size and
+// not far from it by instructions (packed fp32 where it can be): 32 prefixes of 816 tokens,
+// 9 rows of 512 bytes each, move 241 MB.
+template <typename T, typename Pool, int D>
+__global__ void __launch_bounds__(256, 3) k_rows(const __grid_constant__ RowArgs a) {
+  using M = RowMath<T, D>;
+  constexpr int kN = M::kN, kP = M::kP, kLanes = M::kLanes, kGroups = 256 / kLanes, kAhead = 3;
+  __shared__ uint64_t sm_turn[D / 2];  // lanes index it apart: from the parameters that would be one after another
+  __shared__ __align__(16) float sm_gain[D];  // 1 + gain
+  pdl_wait();
+  pdl_trigger();
+  const bool is_q = blockIdx.x < a.q_blocks;
+  const bool to_pages = !is_q && a.to_cache;
+  const uint32_t block = is_q ? blockIdx.x : blockIdx.x - a.q_blocks;
+  const uint32_t item = block * kGroups + threadIdx.x / kLanes;
+  const int l0 = threadIdx.x % kLanes * kN;
+  const FastDiv &by_items = is_q ? a.by_q : a.by_k;  // items of a token
+  const float *gain = is_q ? a.q_gain : a.k_gain;
+  const int heads = is_q ? a.hq : a.hk, per = to_pages ? 1 : min(a.per, heads);
+  const uint32_t tok = by_items.div(item), b = a.by_t.div(tok);
+  const int t = (int)(tok - b * a.T), h0 = (int)(item - tok * by_items.d) * per;
+  const bool inside = item < (uint32_t)a.B * a.T * by_items.d;
+  const bool kept = inside && (!to_pages || !a.count || t < a.count[b]);
+
+  const RowsPtr &in = is_q ? a.q : a.k;
+  const T *src = (const T *)in.data + (kept ? b * in.sb + t * in.st + h0 * in.sh + l0 : 0);
+  const int n = kept ? min(per, heads - h0) : 0;
+  uint4 lo[kAhead], hi[kAhead];
+  auto load = [&](int j, const T *p, bool on) {
+    lo[j] = hi[j] = make_uint4(0, 0, 0, 0);
+    if (on) {
+      lo[j] = *reinterpret_cast<const uint4 *>(p);
+      hi[j] = *reinterpret_cast<const uint4 *>(p + D / 2);
+    }
+  };
+  if (to_pages) {
+    load(0, src, kept);
+    load(1, (const T *)a.v.data + (kept ? b * a.v.sb + t * a.v.st + h0 * a.v.sh + l0 : 0), kept);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      load(j, src, j < n);
+      src += in.sh;
+    }
+  }
+  const int64_t slot = (int64_t)(a.start && kept ? a.start[b] : 0) + t;
+  const int64_t pos = a.positions && kept ? (int64_t)a.positions[tok] : slot;
+  const int cell = to_pages && kept ? cache_row(a.pt, b, slot) : -1;  // row of the pools
+  if (a.rotate)
+    for (int i = threadIdx.x; i < D / 2; i += 256) sm_turn[M::turn_at(i)] = a.turn[i];
+  if (gain)
+    for (int i = threadIdx.x; i < D; i += 256) sm_gain[M::gain_at(i)] = 1.0f + gain[i];
+  if (!__syncthreads_or(kept)) return;
+  M math;
+  if (a.rotate) math.turn(pos, sm_turn + l0 / kN);
+
+  if (!to_pages) {
+    const RowsPtr &to = is_q ? a.q_out : a.k_out;
+    T *dst = (T *)to.data + (kept ? b * to.sb + t * to.st + h0 * to.sh + l0 : 0);
+    for (int r0 = 0; r0 < per; r0 += kAhead) {
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (r0 + j >= per) break;  // the same for all: the exchanges below are warp-wide
+        f32x2 x[kP], y[kP];
+        Vec<T>::get(lo[j], x);
+        Vec<T>::get(hi[j], y);
+        load(j, src, r0 + j + kAhead < n);
+        src += in.sh;
+        if (gain) M::norm(x, y, sm_gain + l0 / kN * 4, a.eps);
+        if (a.rotate) math.rotate(x, y);
+        float u[kN], v[kN];
+        M::floats(x, u);
+        M::floats(y, v);
+        if (r0 + j < n) {
+          *reinterpret_cast<uint4 *>(dst) = Vec<T>::put(u);
+          *reinterpret_cast<uint4 *>(dst + D / 2) = Vec<T>::put(v);
         }
+        dst += to.sh;
       }
     }
-    if (a.rotate && (is_q || is_k)) {
+    return;
+  }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo = x[i] * c[i] - y[i] * s[i];
-        y[i] = y[i] * c[i] + x[i] * s[i];
-        x[i] = lo;
-      }
-    }
-    if constexpr (Pool::kScaled) {  // launched with to_cache only
-      // Largest magnitude as bits: NaN and infinity order above every finite value.
-      uint32_t top = 0;
+  for (int j = 0; j < 2; ++j) {  // the key, the value
+    f32x2 x[kP], y[kP];
+    Vec<T>::get(lo[j], x);
+    Vec<T>::get(hi[j], y);
+    if (j == 0 && gain) M::norm(x, y, sm_gain + l0 / kN * 4, a.eps);
+    if (j == 0 && a.rotate) math.rotate(x, y);
+    float u[kN], v[kN];
+    M::floats(x, u);
+    M::floats(y, v);
+    const PoolPtr &pool = j ? a.vp : a.kp;
+    const int64_t at = (int64_t)cell * a.hk + h0;
+    if constexpr (Pool::kScaled) {
+      float most = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        top = max(top, max(__float_as_uint(x[i]) & 0x7fffffffu, __float_as_uint(y[i]) & 0x7fffffffu));
+      for (int i = 0; i < kN; ++i) most = max_nan(max_nan(most, fabsf(u[i])), fabsf(v[i]));
 #pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
-      if (put && !is_q) {
-        const PoolPtr &pool = is_k ? a.kp : a.vp;
-        const int64_t at = (int64_t)cell * a.hk + h;
+      for (int o = kLanes / 2; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(kFull, most, o));
+      if (cell >= 0) {
+        const uint32_t top = __float_as_uint(most);
         const bool finite = top < 0x7f800000u;
         const float scale = finite ? Pool::scale(top) : __uint_as_float(0x7fc00000u);
-        uint32_t lo = 0, hi = 0;
-        if (finite) {
-          lo = Pool::codes(x, scale);
-          hi = Pool::codes(y, scale);
+        uint32_t w[kN / 4] = {}, w2[kN / 4] = {};
+        if (finite)
+#pragma unroll
+          for (int i = 0; i < kN / 4; ++i) {
+            w[i] = Pool::codes(u + 4 * i, scale);
+            w2[i] = Pool::codes(v + 4 * i, scale);
+          }
+        uint8_t *dst = (uint8_t *)pool.codes + at * D + l0;
+        if constexpr (kN == 8) {
+          *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+          *reinterpret_cast<uint2 *>(dst + D / 2) = make_uint2(w2[0], w2[1]);
+        } else {
+          *reinterpret_cast<uint32_t *>(dst) = w[0];
+          *reinterpret_cast<uint32_t *>(dst + D / 2) = w2[0];
         }
-        uint8_t *dst = (uint8_t *)pool.codes + at * D + l4;
-        *reinterpret_cast<uint32_t *>(dst) = lo;
-        *reinterpret_cast<uint32_t *>(dst + D / 2) = hi;
-        if (l4 == 0) pool.scale[at] = scale;
+        if (l0 == 0) pool.scale[at] = scale;
       }
-    }
-    if (put && (is_q || !a.to_cache)) {
-      const RowsPtr &dst = is_q ? a.q_out : a.k_out;
-      T *p = (T *)dst.data + b * dst.sb + t * dst.st + h * dst.sh + l4;
-      store4(p, x);
-      store4(p + D / 2, y);
-    }
-    if (put && !is_q && a.to_cache && !Pool::kScaled) {
-      bf16 *p = (bf16 *)(is_k ? a.kp : a.vp).codes + ((int64_t)cell * a.hk + h) * D + l4;
-      store4(p, x);
-      store4(p + D / 2, y);
+    } else if (cell >= 0) {
+      bf16 *dst = (bf16 *)pool.codes + at * D + l0;
+      store_bf16(dst, u);
+      store_bf16(dst + D / 2, v);
     }
   }
 }
 
-// A lane group of D/8 lanes moves a row of keys and the row of values beside it.
+// A group of lanes moves a row of keys and the row of values beside it, 16 bytes of
+// output a lane (8 bf16 or 4 fp32 values), and kAtOnce such pairs at once, whose loads are on
+// their way together.  Bound by HBM: 18 layers of 16 prefixes of 560 tokens move 321 MB.
 template <typename T, typename Pool, int D>
 __global__ void __launch_bounds__(256) k_cache_read(const __grid_constant__ ReadArgs a) {
   pdl_wait();
   pdl_trigger();
-  constexpr int kLanes = D / 8;
-  const int64_t items = (int64_t)a.layers * a.B * a.kv * a.P;
-  const int64_t step = (int64_t)gridDim.x * blockDim.x / kLanes;
-  const int l8 = (threadIdx.x % kLanes) * 8;
-  for (int64_t item = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / kLanes; item < items; item += step) {
-    const int p = (int)(item % a.P);
-    const int64_t rest = item / a.P;
-    const int h = (int)(rest % a.kv), b = (int)(rest / a.kv % a.B), layer = (int)(rest / a.kv / a.B);
-    int cell = -1;
-    if (p < a.lens[b] && (!a.mask || a.mask[(int64_t)b * a.P + p])) cell = cache_row(a.pt, b, p);
-    if (a.mask_out && layer == 0 && h == 0 && l8 == 0) a.mask_out[(int64_t)b * a.P + p] = cell >= 0;
-    const int64_t at = (layer * a.layer_rows + cell) * a.kv + h;
+  constexpr int kN = Vec<T>::kN, kLanes = D / kN, kAtOnce = 2, kWords = kN * (Pool::kScaled ? 1 : 2) / 4;
+  const uint32_t items = (uint32_t)a.layers * a.B * a.kv * a.P;  // below 2^31
+  const uint32_t step = gridDim.x * (256 / kLanes);
+  const int l0 = threadIdx.x % kLanes * kN;
+  for (uint32_t first = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes; first < items; first += kAtOnce * step) {
+    int cell[kAtOnce], h[kAtOnce], layer[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const PoolPtr &pool = i ? a.vp : a.kp;
-      float x[4] = {0, 0, 0, 0}, y[4] = {0, 0, 0, 0};
-      if (cell >= 0) {
-        if constexpr (Pool::kScaled) {
-          const uint2 w = *reinterpret_cast<const uint2 *>((const uint8_t *)pool.codes + at * D + l8);
-          const float scale = pool.scale[at];
-          Pool::values(w.x, x);
-          Pool::values(w.y, y);
+    for (int u = 0; u < kAtOnce; ++u) {
+      const uint32_t item = first + u * step;
+      cell[u] = -1;
+      if (item < items) {
+        const uint32_t rest = a.by_p.div(item), up = a.by_kv.div(rest);
+        layer[u] = (int)a.by_b.div(up);
+        h[u] = (int)(rest - up * a.kv);
+        const int p = (int)(item - rest * a.P), b = (int)(up - layer[u] * a.B);
+        if (p < a.lens[b] && (!a.mask || a.mask[(int64_t)b * a.P + p])) cell[u] = cache_row(a.pt, b, p);
+        if (a.mask_out && layer[u] == 0 && h[u] == 0 && l0 == 0) a.mask_out[(int64_t)b * a.P + p] = cell[u] >= 0;
+      }
+    }
+    uint32_t w[kAtOnce][2][kWords];  // codes of the lane's values
+    float scale[kAtOnce][2];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] *= scale, y[j] *= scale;
-        } else {
-          load4((const bf16 *)pool.codes + at * D + l8, x);
-          load4((const bf16 *)pool.codes + at * D + l8 + 4, y);
+    for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) w[u][i][j] = 0;
+        scale[u][i] = 0.0f;
+        if (cell[u] >= 0) {
+          const PoolPtr &pool = i ? a.vp : a.kp;
+          const int64_t at = (layer[u] * a.layer_rows + cell[u]) * a.kv + h[u];
+          const uint8_t *p = (const uint8_t *)pool.codes + (at * D + l0) * (Pool::kScaled ? 1 : 2);
+          if constexpr (kWords == 4)
+            *reinterpret_cast<uint4 *>(w[u][i]) = *reinterpret_cast<const uint4 *>(p);
+          else if constexpr (kWords == 2)
+            *reinterpret_cast<uint2 *>(w[u][i]) = *reinterpret_cast<const uint2 *>(p);
+          else
+            w[u][i][0] = *reinterpret_cast<const uint32_t *>(p);
+          if constexpr (Pool::kScaled) scale[u][i] = pool.scale[at];
         }
       }
-      T *dst = (T *)(i ? a.v_out : a.k_out) + item * D + l8;
-      store4(dst, x);
-      store4(dst + 4, y);
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const uint32_t item = first + u * step;
+      if (item >= items) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float x[kN];
+        if constexpr (Pool::kScaled) {
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) Pool::values(w[u][i][j], x + 4 * j);
+#pragma unroll
+          for (int j = 0; j < kN; ++j) x[j] *= scale[u][i];
+        } else {
+#pragma unroll
+          for (int j = 0; j < kWords; ++j)
+            x[2 * j] = __uint_as_float(w[u][i][j] << 16), x[2 * j + 1] = __uint_as_float(w[u][i][j] & 0xffff0000u);
+        }
+        *reinterpret_cast<uint4 *>((T *)(i ? a.v_out : a.k_out) + (int64_t)item * D + l0) = Vec<T>::put(x);
+      }
     }
   }
 }
@@ -257,17 +437,29 @@ namespace {
 
 template <typename T, typename Pool, int D>
 cudaError_t rows_go(RowArgs a, cudaStream_t s) {
-  constexpr int kLanes = D / 8;
-  const int rows = a.hq + a.hk + a.hv;
-  a.per = 1;
-  const int64_t threads = (int64_t)a.B * a.T * ((rows + a.per - 1) / a.per) * kLanes;
-  return launch_pdl(k_rows<T, Pool, D>, dim3((unsigned)((threads + 255) / 256)), 256, 0, s, a);
+  constexpr uint32_t kGroups = 256 / RowMath<T, D>::kLanes;
+  const uint32_t tokens = (uint32_t)a.B * a.T;
+  // Heads of an item: all of a token's (up to 16) where there are enough tokens for two
+  // blocks an SM, one where there are few.
+  const uint32_t most = (uint32_t)((uint64_t)tokens * (a.hq + a.hk) / (148 * 2 * kGroups));
+  a.per = most < 1 ? 1 : most > 16 ? 16 : (int)most;
+  auto items = [&](int heads, int per) { return (uint32_t)((heads + per - 1) / per); };
+  auto blocks = [&](uint32_t n) { return (tokens * n + kGroups - 1) / kGroups; };
+  const uint32_t nq = items(a.hq, a.per), nk = items(a.hk, a.to_cache ? 1 : a.per);
+  a.by_q = FastDiv(nq ? nq : 1);
+  a.by_k = FastDiv(nk ? nk : 1);
+  a.by_t = FastDiv(a.T);
+  a.q_blocks = blocks(nq);
+  return launch_pdl(k_rows<T, Pool, D>, dim3(a.q_blocks + blocks(nk)), 256, 0, s, a);
 }
 template <typename T, typename Pool, int D>
-cudaError_t read_go(const ReadArgs &a, cudaStream_t s) {
-  const int64_t threads = (int64_t)a.layers * a.B * a.kv * a.P * (D / 8);
+cudaError_t read_go(ReadArgs a, cudaStream_t s) {
+  a.by_p = FastDiv(a.P);
+  a.by_kv = FastDiv(a.kv);
+  a.by_b = FastDiv(a.B);
+  const int64_t threads = (int64_t)a.layers * a.B * a.kv * a.P * (D / Vec<T>::kN);
   const int64_t blocks = (threads + 255) / 256;
-  return launch_pdl(k_cache_read<T, Pool, D>, dim3((unsigned)(blocks < 148 * 32 ? blocks : 148 * 32)), 256, 0, s, a);
+  return launch_pdl(k_cache_read<T, Pool, D>, dim3((unsigned)(blocks < 148 * 16 ? blocks : 148 * 16)), 256, 0, s, a);
 }
 
 #define PI0X_PICK(fn, ...)                                                                    \

@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) k_attend(const __gr
         k.page[r] = -1;
         k.on[r] = 1;
         if (i < S::kKeys && p < key_end) {
-          k.page[r] = a.pt.table[(int64_t)b * a.pt.max_pages + (uint32_t)p / (uint32_t)a.pt.page_size];
+          k.page[r] = a.pt.table[(int64_t)b * a.pt.max_pages + a.pt.by_page.div((uint32_t)p)];
           if (a.mask) k.on[r] = a.mask[(int64_t)b * a.mask_len + p];
         }
       }
@@ -314,7 +314,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) k_attend(const __gr
 #pragma unroll
       for (int r = 0; r < kRegs; ++r) {
         const bool ok = k.on[r] && k.page[r] >= 0 && k.page[r] < a.pt.num_pages;
-        st.rows[r] = ok ? k.page[r] * a.pt.page_size + (int)((uint32_t)(key + r * 32 + lane) % (uint32_t)a.pt.page_size) : -1;
+        const uint32_t p = key + r * 32 + lane, off = p - a.pt.by_page.div(p) * a.pt.page_size;
+        st.rows[r] = ok ? k.page[r] * a.pt.page_size + (int)off : -1;
         st.seen[r] = __ballot_sync(kFull, ok);
         st.ks[r] = st.vs[r] = 0.0f;
         if constexpr (C::kScaled)
