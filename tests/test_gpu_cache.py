@@ -375,6 +375,9 @@ def check_attend(c, layer, q, table, lens, mask, scale, out, lse):
     (1, 33, 1, 128, 32, [700]),
     (130, 8, 1, 64, 16, [i * 5 % 97 for i in range(130)]),
     (1, 8, 1, 256, 64, [20000]),
+    (400, 8, 1, 256, 16, [i * 37 % 701 for i in range(400)]),        # more units than CTAs, evenly split and joined
+    (6, 12, 2, 128, 64, [9000, 0, 1, 30000, 17000, 64]),            # a few long ones: units over many CTAs
+    (33, 3, 3, 256, 32, [i * 53 % 2000 for i in range(33)]),
 ])
 def test_attend_matches_the_formula(pool, B, H, kv, D, ps, lens):
     g = rng(sum(lens) % 1000 + D)

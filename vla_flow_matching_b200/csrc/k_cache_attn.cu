@@ -28,8 +28,10 @@ namespace pi0x {
 namespace {
 constexpr int kWarps = 4;
 constexpr int kHeadsPerUnit = 8;  // query heads of one kv head that share a pass: the product's columns
-constexpr int kBlocksPerSm = 2, kMaxGrid = 148 * kBlocksPerSm;
+constexpr int kMaxGrid = 148 * 3;
 constexpr int kJoinThreads = 512;
+constexpr float kWeightBits = 15.0f;
+constexpr int kMaxCluster = 8, kClusterBlocks = 8;
 constexpr unsigned kFull = 0xffffffffu;
 
 // Four 8x8 matrices of 16-bit elements, lane i's address the row i % 8 of matrix i / 8.
@@ -51,6 +53,28 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
+}
+// Distributed shared memory: all threads of the cluster, and the address of a peer's copy of a variable.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t at_peer(const void *p, uint32_t rank) {
+  uint32_t d;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_u32(p)), "r"(rank));
+  return d;
+}
+__device__ __forceinline__ float peer_load(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_load4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 // What the lane that keeps key i of 16-key tile u holds.
 template <typename V, int N>
@@ -121,7 +145,7 @@ struct Shape {
   static constexpr int kPitch = kRowBytes + 16;  // 8 rows of a matrix fall into different banks
   // keys a warp takes at once: 16 per product, more where rows are short, so that a buffer
   // holds 8 KB (4 KB at 64 bytes a row)
-  static constexpr int kTiles = kRowBytes >= 512 ? 1 : kRowBytes >= 256 ? 2 : 4;
+  static constexpr int kTiles = kRowBytes >= 512 ? 1 : 2;
   static constexpr int kKeys = 16 * kTiles;
   static constexpr int kBlock = kWarps * kKeys;  // keys of a scheduling block
   static constexpr int kMTiles = D / 16;
@@ -130,13 +154,28 @@ struct Shape {
   static constexpr int kHeadPitch = D + 4;       // floats: the warps' sums on their way to each other
   static_assert(kHeadsPerUnit * kHeadPitch * 4 <= kRing, "a warp's sums fit its ring");
   static constexpr int kSmem = kWarps * kRing;
+  static constexpr int kBlocksPerSm = kRowBytes >= 256 ? 2 : 3;
+  static constexpr int kGrid = 148 * kBlocksPerSm;
 };
 
 // Work: units u = (sample, kv head, group of up to 8 query heads), each of ceil(len/kBlock)
-// blocks of keys (at least one), laid end to end and shared out evenly over the grid: a CTA
-// takes `share` consecutive blocks, whichever units they belong to.  A unit inside one CTA is
-// finished there; of a longer one every CTA leaves its part (m, l and the unnormalised sum) in
-// the workspace, and k_attend_join adds them up in order.
+// blocks of keys (at least one).  Two ways to share them out:
+//  * kCluster: a cluster of 1 to 8 CTAs takes a unit, its CTAs in turn a block each, and adds
+//    up the CTAs' sums through distributed shared memory.  One launch, no workspace, and a CTA
+//    knows its first keys before it knows the sample's length, so that page numbers, mask, q
+//    and length are on their way together.
+//  * else the units are laid end to end and a CTA takes an equal share of all blocks,
+//    whichever units they belong to.  A unit inside one CTA is finished there; of a longer one
+//    every CTA leaves its part (m, l and the unnormalised sum) in the workspace, and
+//    k_attend_join adds them up in order.
+// attend_go() has the choice between them.  Split units are listed in the workspace: by unit
+// if there are no more units than CTAs, else by the CTA that a unit starts in (each CTA starts
+// at most one that goes on).
+struct __align__(16) Split {
+  int unit;         // -1: none here
+  int first, last;  // its CTAs
+  int slot;         // the first CTA's part; that of CTA c > first is 2c
+};
 template <int N>
 struct Look {
   int page[N];
@@ -148,15 +187,6 @@ struct Step {
   unsigned seen[N];      // a bit for each visible key
   float ks[N], vs[N];    // 8-bit codes: scales
 };
-//
-// Split units are listed in the workspace: by unit if there are no more units than CTAs,
-// else by the CTA that a unit starts in (each CTA starts at most one that goes on).
-struct __align__(16) Split {
-  int unit;         // -1: none here
-  int first, last;  // its CTAs
-  int slot;         // the first CTA's part; that of CTA c > first is 2c
-};
-
 __device__ __forceinline__ int keys_of(const AttendArgs &a, int b) {
   int64_t n = a.lens[b];
   n = min(n, (int64_t)a.pt.max_pages * a.pt.page_size);
@@ -170,69 +200,110 @@ constexpr int kPartFloats = kHeadsPerUnit * D + 2 * kHeadsPerUnit;
 
 }  // namespace
 
-template <typename C, int D>
-__global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) k_attend(const __grid_constant__ AttendArgs a) {
+template <typename C, int D, bool kCluster>
+__global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
+    k_attend(const __grid_constant__ AttendArgs a, int cluster) {
   using S = Shape<C, D>;
   pdl_wait();
   pdl_trigger();
   extern __shared__ __align__(16) uint8_t sm_ring[];
   __shared__ __align__(16) uint8_t sm_q[kHeadsPerUnit][D * 2 + 16];
   __shared__ float sm_m[kWarps][kHeadsPerUnit], sm_l[kWarps][kHeadsPerUnit], sm_qf[kHeadsPerUnit];
-  __shared__ int sm_scan[kWarps], sm_b, sm_at;
+  __shared__ float sm_ml[2][kHeadsPerUnit];  // kCluster: this CTA's m and l
+  __shared__ int64_t sm_scan[kWarps], sm_at;
+  __shared__ int sm_b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int group = a.heads / a.kv, groups = head_groups(a.heads, a.kv), upb = a.kv * groups;
+  auto blocks_of = [](int len) { return max(1, (int)(((uint32_t)len + S::kBlock - 1) / S::kBlock)); };
 
-  // ---- this CTA's blocks [c0, c1) of all blocks, and the sample the first lies in
-  auto blocks_of = [&](int b) { return max(1, (keys_of(a, b) + S::kBlock - 1) / S::kBlock); };
-  const int per = (a.B + kWarps * 32 - 1) / (kWarps * 32), b_lo = min(a.B, tid * per), b_hi = min(a.B, b_lo + per);
-  int mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += blocks_of(b);
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) sm_scan[warp] = incl;
-  __syncthreads();
-  int before = 0, total_b = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sm_scan[w];
-    total_b += sm_scan[w];
-  }
-  const int64_t total = (int64_t)total_b * upb;
-  const int64_t share = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t c0 = min(total, blockIdx.x * share), c1 = min(total, c0 + share);
+  // ---- this CTA's blocks [c0, c1), its first sample, and where in the sample's units it starts
+  int b;
+  int64_t c0, c1, at, total = 1, ctas = 1;
   Split *splits = reinterpret_cast<Split *>(a.part);
   float *parts = a.part + gridDim.x * (sizeof(Split) / 4);
   const bool by_unit = (int64_t)a.B * upb <= gridDim.x;
-  if (!by_unit && tid == 0) splits[blockIdx.x].unit = -1;
-  {
-    int64_t off = (int64_t)(before + incl - mine) * upb;
-    if (c0 < c1 && c0 >= off && c0 < off + (int64_t)mine * upb) {
-      int b = b_lo;
-      for (;; ++b) {
-        const int64_t n = (int64_t)blocks_of(b) * upb;
+  const int rank = kCluster ? (int)(blockIdx.x % cluster) : 0;
+  if constexpr (kCluster) {
+    b = blockIdx.x / cluster / upb;
+    c0 = c1 = at = 0;
+  } else {
+    const int per = (a.B + kWarps * 32 - 1) / (kWarps * 32), b_lo = min(a.B, tid * per), b_hi = min(a.B, b_lo + per);
+    int64_t mine = 0;
+    for (int i = b_lo; i < b_hi; ++i) mine += blocks_of(keys_of(a, i));
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sm_scan[warp] = incl;
+    __syncthreads();
+    int64_t before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sm_scan[w];
+      total += sm_scan[w];
+    }
+    total *= upb;
+    ctas = min((int64_t)gridDim.x, total);  // with at least a block each
+    c0 = min(total, blockIdx.x * total / ctas);
+    c1 = min(total, (blockIdx.x + 1) * total / ctas);
+    if (!by_unit && tid == 0) splits[blockIdx.x].unit = -1;
+    int64_t off = (before + incl - mine) * upb;
+    if (c0 < c1 && c0 >= off && c0 < off + mine * upb) {
+      int i = b_lo;
+      for (;; ++i) {
+        const int64_t n = (int64_t)blocks_of(keys_of(a, i)) * upb;
         if (c0 < off + n) break;
         off += n;
       }
-      sm_b = b;
-      sm_at = (int)(c0 - off);  // blocks into the sample's units
+      sm_b = i;
+      sm_at = c0 - off;  // blocks into the sample's units
     }
+    __syncthreads();
+    if (c0 >= c1) return;
+    b = sm_b;
+    at = sm_at;
   }
-  __syncthreads();
-  if (c0 >= c1) return;
-  int b = sm_b;
-  int64_t at = sm_at;
 
   // ---- one segment after another: the blocks of one unit that are this CTA's
-  for (int64_t c = c0; c < c1;) {
-    const int len = keys_of(a, b), nblk = blocks_of(b);
-    const int ub = (int)(at / nblk), blk0 = (int)(at - (int64_t)ub * nblk);
-    const int nseg = (int)min((int64_t)(nblk - blk0), c1 - c);
+  for (int64_t c = c0;;) {
+    constexpr int kRegs = (S::kKeys + 31) / 32;  // a lane keeps key i of a step, and key 32 + i of longer ones
+    int len = 0, nblk = 1, ub, blk0 = 0, nseg = 0, key_0, key_end, look_end;
+    const int hop = kCluster ? cluster * S::kBlock : S::kBlock;  // from a step's keys to the next's
+    if constexpr (kCluster) {
+      ub = (int)(blockIdx.x / cluster) - b * upb;
+      key_0 = rank * S::kBlock + warp * S::kKeys;
+      look_end = a.mask ? min(a.mask_len, a.pt.max_pages * a.pt.page_size) : a.pt.max_pages * a.pt.page_size;
+    } else {
+      len = keys_of(a, b), nblk = blocks_of(len);
+      ub = (int)(at / nblk), blk0 = (int)(at - (int64_t)ub * nblk);
+      nseg = (int)min((int64_t)(nblk - blk0), c1 - c);
+      key_0 = blk0 * S::kBlock + warp * S::kKeys;
+      look_end = key_end = (int)min((int64_t)len, ((int64_t)blk0 + nseg) * S::kBlock);
+    }
     const int h = ub / groups, h0 = h * group + (ub % groups) * kHeadsPerUnit;
     const int nh = min(kHeadsPerUnit, group - (ub % groups) * kHeadsPerUnit);
+
+    // look() issues the loads of a step's page numbers and mask, settle(), a step later, takes
+    // what came.  Unseen keys are not read: their rows are filled with zeros.
+    auto look = [&](int key) {
+      Look<kRegs> k;
+#pragma unroll
+      for (int r = 0; r < kRegs; ++r) {
+        const int i = r * 32 + lane, p = key + i;
+        k.page[r] = -1;
+        k.on[r] = 1;
+        if (i < S::kKeys && p < look_end) {
+          k.page[r] = a.pt.table[(int64_t)b * a.pt.max_pages + a.pt.by_page.div((uint32_t)p)];
+          if (a.mask) k.on[r] = a.mask[(int64_t)b * a.mask_len + p];
+        }
+      }
+      return k;
+    };
+    Look<kRegs> k0 = look(key_0), ahead = look(key_0 + hop);
+    if constexpr (kCluster) key_end = len = keys_of(a, b);
 
     // q: 16 threads a head.  fp16 products take q times a power of two (so that the largest
     // element is in [1, 2)): exact for all that matters of a bf16 q.
@@ -283,38 +354,20 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) k_attend(const __gr
     const uint32_t row_bytes = (uint32_t)a.kv * S::kRowBytes;
     const uint8_t *kbase = (const uint8_t *)a.kp.codes + (int64_t)h * S::kRowBytes;
     const uint8_t *vbase = (const uint8_t *)a.vp.codes + (int64_t)h * S::kRowBytes;
-    const int key_end = min(len, (blk0 + nseg) * S::kBlock);
-    const int key_0 = blk0 * S::kBlock + warp * S::kKeys;
-    constexpr int kRegs = (S::kKeys + 31) / 32;  // a lane keeps key i of a step, and key 32 + i of longer ones
 
     float o[S::kMTiles][4];
 #pragma unroll
     for (int i = 0; i < S::kMTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-    float w0 = -INFINITY, w1 = -INFINITY;  // 8-bit codes: running maximum of s + log2(value scale)
+    float w0 = -INFINITY, w1 = -INFINITY;  // 8-bit codes: running maximum of s + log2(value scale) - 15
 
-    // look() issues the loads of a step's page numbers and mask, settle(), a step later, takes
-    // what came.  Unseen keys are not read: their rows are filled with zeros.
-    auto look = [&](int key) {
-      Look<kRegs> k;
-#pragma unroll
-      for (int r = 0; r < kRegs; ++r) {
-        const int i = r * 32 + lane, p = key + i;
-        k.page[r] = -1;
-        k.on[r] = 1;
-        if (i < S::kKeys && p < key_end) {
-          k.page[r] = a.pt.table[(int64_t)b * a.pt.max_pages + a.pt.by_page.div((uint32_t)p)];
-          if (a.mask) k.on[r] = a.mask[(int64_t)b * a.mask_len + p];
-        }
-      }
-      return k;
-    };
     auto settle = [&](const Look<kRegs> &k, int key) {
       Step<kRegs> st;
 #pragma unroll
       for (int r = 0; r < kRegs; ++r) {
-        const bool ok = k.on[r] && k.page[r] >= 0 && k.page[r] < a.pt.num_pages;
-        const uint32_t p = key + r * 32 + lane, off = p - a.pt.by_page.div(p) * a.pt.page_size;
+        const uint32_t p = key + r * 32 + lane;
+        const bool ok = k.on[r] && k.page[r] >= 0 && k.page[r] < a.pt.num_pages && (!kCluster || (int)p < key_end);
+        const uint32_t off = p - a.pt.by_page.div(p) * a.pt.page_size;
         st.rows[r] = ok ? k.page[r] * a.pt.page_size + (int)off : -1;
         st.seen[r] = __ballot_sync(kFull, ok);
         st.ks[r] = st.vs[r] = 0.0f;
@@ -340,7 +393,6 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) k_attend(const __gr
     };
     auto next_buf = [](int buf) { return buf == 2 ? 0 : buf + 1; };
 
-    Look<kRegs> k0 = look(key_0), ahead = look(key_0 + S::kBlock);
     Step<kRegs> now = settle(k0, key_0);
     int kbuf = 0;
     if (key_0 < key_end) {
@@ -349,11 +401,11 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) k_attend(const __gr
       copy(now, vbase, 1);
       cp_async_commit();
     }
-    Step<kRegs> next = settle(ahead, key_0 + S::kBlock);
-    if (key_0 + S::kBlock < key_end) copy(next, kbase, 2);
+    Step<kRegs> next = settle(ahead, key_0 + hop);
+    if (key_0 + hop < key_end) copy(next, kbase, 2);
     cp_async_commit();
-    ahead = look(key_0 + 2 * S::kBlock);
-    for (int key = key_0; key < key_end; key += S::kBlock) {
+    ahead = look(key_0 + 2 * hop);
+    for (int key = key_0; key < key_end; key += hop) {
       // committed by now: this step's K and V and the next one's K
       cp_async_wait<2>();
       __syncwarp();
@@ -390,7 +442,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) k_attend(const __gr
         if (!(seen >> 8 & 1)) s[u][2] = s[u][3] = -INFINITY;
       }
       __syncwarp();
-      if (key + S::kBlock < key_end) copy(next, vbase, kbuf);  // the next step's V takes K's buffer
+      if (key + hop < key_end) copy(next, vbase, kbuf);  // the next step's V takes K's buffer
       cp_async_commit();
       const int vbuf = next_buf(kbuf);
 
@@ -419,9 +471,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) k_attend(const __gr
         l1 += p[u][1] + p[u][3];
       }
       if constexpr (C::kScaled) {
-        // A value's scale goes into its weight: 2^(s + log2 scale - w) with a maximum w of its
-        // own, which keeps the fp16 weights in range whatever the scales are.
-        float e0 = w0, e1 = w1, lv[kRegs];
+        // A value's scale goes into its weight: 2^(s + log2 scale - w + 15) with a maximum w of
+        // its own, which keeps the fp16 weights in range whatever the scales are: the largest is
+        // 2^15, and one of 2^-29 of it still has all 11 bits.
+        float e0 = w0 + kWeightBits, e1 = w1 + kWeightBits, lv[kRegs];
 #pragma unroll
         for (int r = 0; r < kRegs; ++r) lv[r] = log2_approx(now.vs[r]);
 #pragma unroll
@@ -436,6 +489,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) k_attend(const __gr
           e0 = fmaxf(e0, __shfl_xor_sync(kFull, e0, d));
           e1 = fmaxf(e1, __shfl_xor_sync(kFull, e1, d));
         }
+        e0 -= kWeightBits, e1 -= kWeightBits;
         const float y0 = e0 == -INFINITY ? 0.0f : e0, y1 = e1 == -INFINITY ? 0.0f : e1;
         f0 = ex2_approx(w0 - y0), f1 = ex2_approx(w1 - y1);
         w0 = e0, w1 = e1;
@@ -480,10 +534,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) k_attend(const __gr
       }
       __syncwarp();
       now = next;
-      next = settle(ahead, key + 2 * S::kBlock);
-      if (key + 2 * S::kBlock < key_end) copy(next, kbase, vbuf);  // the K after the next takes V's buffer
+      next = settle(ahead, key + 2 * hop);
+      if (key + 2 * hop < key_end) copy(next, kbase, vbuf);  // the K after the next takes V's buffer
       cp_async_commit();
-      ahead = look(key + 3 * S::kBlock);
+      ahead = look(key + 3 * hop);
       kbuf = next_buf(vbuf);
     }
 
@@ -518,9 +572,16 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) k_attend(const __gr
       }
     }
     __syncthreads();
-    const bool whole = nseg == nblk;
+    const bool whole = kCluster ? cluster == 1 : nseg == nblk;
     const int slot = 2 * (int)blockIdx.x + (c > c0);
     float *part = parts + (int64_t)slot * kPartFloats<D>;
+    auto finish = [&](int n, int d, const float4 &x, float m, float l) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const int64_t at_out = ((int64_t)b * a.heads + h0 + n);
+      *reinterpret_cast<uint2 *>(a.out + at_out * D + d) =
+          make_uint2(CodeBf16::pack(x.x * inv, x.y * inv), CodeBf16::pack(x.z * inv, x.w * inv));
+      if (d == 0 && a.lse) a.lse[at_out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    };
     for (int i = tid; i < nh * (D / 4); i += kWarps * 32) {
       const int n = i / (D / 4), d = i % (D / 4) * 4;
       float mm = sm_m[0][n];
@@ -536,27 +597,56 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocksPerSm) k_attend(const __gr
         l += f * sm_l[w][n];
       }
       if (whole) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const int64_t at_out = ((int64_t)b * a.heads + h0 + n);
-        *reinterpret_cast<uint2 *>(a.out + at_out * D + d) =
-            make_uint2(CodeBf16::pack(x.x * inv, x.y * inv), CodeBf16::pack(x.z * inv, x.w * inv));
-        if (d == 0 && a.lse) a.lse[at_out] = l == 0.0f ? -INFINITY : (mm + log2f(l)) * 0.6931471805599453f;
+        finish(n, d, x, mm, l);
+      } else if constexpr (kCluster) {  // over warp 0's sum, which this thread alone has read
+        *reinterpret_cast<float4 *>(sm_ring + (n * S::kHeadPitch + d) * 4) = x;
+        if (d == 0) sm_ml[0][n] = mm, sm_ml[1][n] = l;
       } else {
         *reinterpret_cast<float4 *>(part + n * D + d) = x;
         if (d == 0) part[kHeadsPerUnit * D + 2 * n] = mm, part[kHeadsPerUnit * D + 2 * n + 1] = l;
       }
     }
+    if constexpr (kCluster) {
+      if (whole) return;
+      cluster_sync();
+      for (int i = rank * kWarps * 32 + tid; i < nh * (D / 4); i += cluster * kWarps * 32) {
+        const int n = i / (D / 4), d = i % (D / 4) * 4;
+        float m[kMaxCluster], mm = -INFINITY, l = 0.0f;
+        float4 x = make_float4(0, 0, 0, 0), y[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          m[r] = -INFINITY;
+          if (r < cluster) {
+            m[r] = peer_load(at_peer(&sm_ml[0][n], r));
+            y[r] = peer_load4(at_peer(sm_ring + (n * S::kHeadPitch + d) * 4, r));
+          }
+          mm = fmaxf(mm, m[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < cluster) {
+            const float f = m[r] == -INFINITY ? 0.0f : ex2_approx(m[r] - mm);
+            x.x += f * y[r].x, x.y += f * y[r].y, x.z += f * y[r].z, x.w += f * y[r].w;
+            l += f * peer_load(at_peer(&sm_ml[1][n], r));
+          }
+        finish(n, d, x, mm, l);
+      }
+      cluster_sync();  // nobody leaves while a peer may read from it
+      return;
+    }
     if (blk0 == 0 && tid == 0) {
       const int unit = b * upb + ub;
       if (!whole)
-        splits[by_unit ? unit : blockIdx.x] = Split{unit, (int)blockIdx.x, (int)((c + nblk - 1) / share), slot};
+        splits[by_unit ? unit : blockIdx.x] =
+            Split{unit, (int)blockIdx.x, (int)(((c + nblk) * ctas - 1) / total), slot};
       else if (by_unit && gridDim.x > 1)  // a lone CTA has no workspace and no second kernel
         splits[unit].unit = -1;
     }
-    __syncthreads();
     c += nseg;
+    if (c >= c1) break;
     at += nseg;
     if (at == (int64_t)nblk * upb) at = 0, ++b;
+    __syncthreads();
   }
 }
 
@@ -654,31 +744,63 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
 
 namespace {
 
-// CTAs of a call: as many as are resident at once, or the blocks of keys there can be.
+// How a call is shared out (see above).  A cluster's CTAs may get more blocks than an even
+// share, if its unit is long for 8 of them; the even way pays for its scan, its parts and the
+// second kernel, about as much as three blocks of a CTA.  Clusters where that is the larger
+// cost, and only while the even share is small: with more work the second kernel is hidden
+// and ragged samples keep the CTAs of a cluster waiting (lengths are not known here: the
+// page tables' are taken).  GPU time of a call, clusters against even shares: 1 x 816 bf16
+// keys XXX, 128 x 600-816 YYY, 1 x 4096 ZZZ us.
+struct Plan {
+  int cluster;  // CTAs of a cluster, 0: even shares and a join
+  int grid;
+};
 template <typename C, int D>
-int attend_grid(int B, int heads, int kv, int page_size, int max_pages) {
+Plan attend_plan(int B, int heads, int kv, int page_size, int max_pages) {
   using S = Shape<C, D>;
-  const int64_t cap = (int64_t)page_size * max_pages;
-  const int64_t most = (int64_t)B * kv * head_groups(heads, kv) * ((cap + S::kBlock - 1) / S::kBlock);
-  return (int)(most < kMaxGrid ? most : kMaxGrid);
+  const int64_t blocks = ((int64_t)page_size * max_pages + S::kBlock - 1) / S::kBlock;
+  const int64_t units = (int64_t)B * kv * head_groups(heads, kv);
+  int cluster = 1;
+  while (cluster < kMaxCluster && cluster < blocks && units * cluster * 2 <= S::kGrid) cluster *= 2;
+  const int64_t even = (units * blocks + S::kGrid - 1) / S::kGrid, mine = (blocks + cluster - 1) / cluster;
+  if (even <= kClusterBlocks && mine <= even + 3) return Plan{cluster, (int)(units * cluster)};
+  return Plan{0, (int)(units * blocks < S::kGrid ? units * blocks : S::kGrid)};
 }
 template <typename C, int D>
 size_t attend_bytes(int B, int heads, int kv, int page_size, int max_pages) {
-  const size_t grid = attend_grid<C, D>(B, heads, kv, page_size, max_pages);
-  return grid > 1 ? grid * (sizeof(Split) + 2 * kPartFloats<D> * sizeof(float)) : 0;
+  const Plan p = attend_plan<C, D>(B, heads, kv, page_size, max_pages);
+  return p.cluster || p.grid == 1 ? 0 : p.grid * (sizeof(Split) + 2 * kPartFloats<D> * sizeof(float));
 }
 template <typename C, int D>
 cudaError_t attend_go(const AttendArgs &a, cudaStream_t s) {
-  const int grid = attend_grid<C, D>(a.B, a.heads, a.kv, a.pt.page_size, a.pt.max_pages);
   using S = Shape<C, D>;
-  cudaError_t e = cudaFuncSetAttribute(k_attend<C, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-  if (e == cudaSuccess) e = launch_pdl(k_attend<C, D>, dim3(grid), kWarps * 32, S::kSmem, s, a);
-  if (e != cudaSuccess || grid == 1) return e;  // one CTA: nothing is split
+  const Plan p = attend_plan<C, D>(a.B, a.heads, a.kv, a.pt.page_size, a.pt.max_pages);
+  if (p.cluster) {
+    cudaError_t e = cudaFuncSetAttribute(k_attend<C, D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.grid);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_attend<C, D, true>, a, p.cluster);
+  }
+  cudaError_t e = cudaFuncSetAttribute(k_attend<C, D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e == cudaSuccess) e = launch_pdl(k_attend<C, D, false>, dim3(p.grid), kWarps * 32, S::kSmem, s, a, 0);
+  if (e != cudaSuccess || p.grid == 1) return e;  // one CTA: nothing is split
   const int64_t units = (int64_t)a.B * a.kv * head_groups(a.heads, a.kv);
-  const int lists = (int)(units < grid ? units : grid);
+  const int lists = (int)(units < p.grid ? units : p.grid);
   int shares = 1;  // about one CTA an SM in all, 16 vectors or more each
   while (shares < D / 8 && lists * shares < 148) shares *= 2;
-  return launch_pdl(k_attend_join<D>, dim3(lists, shares), kJoinThreads, 0, s, a, grid);
+  return launch_pdl(k_attend_join<D>, dim3(lists, shares), kJoinThreads, 0, s, a, p.grid);
 }
 
 #define PI0X_PICK(fn, dtype, dim, ...)                                                                      \
