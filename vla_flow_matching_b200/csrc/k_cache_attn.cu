@@ -23,6 +23,8 @@
 
 #include <math.h>
 
+#include <atomic>
+
 namespace pi0x {
 
 namespace {
@@ -771,12 +773,23 @@ size_t attend_bytes(int B, int heads, int kv, int page_size, int max_pages) {
   const Plan p = attend_plan<C, D>(B, heads, kv, page_size, max_pages);
   return p.cluster || p.grid == 1 ? 0 : p.grid * (sizeof(Split) + 2 * kPartFloats<D> * sizeof(float));
 }
+// Dynamic shared memory beyond 48 KB has to be asked for once a device and kernel.
+template <typename C, int D, bool kCluster>
+cudaError_t allow_smem() {
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && allowed.load(std::memory_order_relaxed) >> dev & 1)) return e;
+  e = cudaFuncSetAttribute(k_attend<C, D, kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<C, D>::kSmem);
+  if (e == cudaSuccess && dev < 64) allowed.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
+}
 template <typename C, int D>
 cudaError_t attend_go(const AttendArgs &a, cudaStream_t s) {
   using S = Shape<C, D>;
   const Plan p = attend_plan<C, D>(a.B, a.heads, a.kv, a.pt.page_size, a.pt.max_pages);
   if (p.cluster) {
-    cudaError_t e = cudaFuncSetAttribute(k_attend<C, D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    const cudaError_t e = allow_smem<C, D, true>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.grid);
@@ -793,7 +806,7 @@ cudaError_t attend_go(const AttendArgs &a, cudaStream_t s) {
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, k_attend<C, D, true>, a, p.cluster);
   }
-  cudaError_t e = cudaFuncSetAttribute(k_attend<C, D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  cudaError_t e = allow_smem<C, D, false>();
   if (e == cudaSuccess) e = launch_pdl(k_attend<C, D, false>, dim3(p.grid), kWarps * 32, S::kSmem, s, a, 0);
   if (e != cudaSuccess || p.grid == 1) return e;  // one CTA: nothing is split
   const int64_t units = (int64_t)a.B * a.kv * head_groups(a.heads, a.kv);

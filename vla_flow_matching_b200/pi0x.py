@@ -2,6 +2,7 @@
 
 Every step of the denoising loop runs in the library's CUDA kernels; this module
 only converts numpy arrays / torch tensors to pointers and checks status codes.
+The paged-cache calls are marshalled in C (csrc/binding.c), the others by ctypes.
 It raises if the shared library is missing: there is no CPU fallback.
 """
 from __future__ import annotations
@@ -88,11 +89,16 @@ class Rotation(ctypes.Structure):
 
 
 _lib = None
+_native = None  # the paged-cache calls' marshalling, csrc/binding.c
+
+
+def _fail(status: int, what: str):
+    raise Pi0xError(status, what)
 
 
 def load() -> ctypes.CDLL:
     """Load libpi0x.so (built in-tree by vla_flow_matching_b200.build)."""
-    global _lib
+    global _lib, _native
     if _lib is not None:
         return _lib
     if not os.path.exists(_LIB_PATH):
@@ -154,6 +160,10 @@ def load() -> ctypes.CDLL:
     lib.pi0x_cache_attention_workspace.restype = ctypes.c_size_t
     lib.pi0x_sample_cache.argtypes = [ptr, cache, cint, cint, ptr, cint, ptr, ptr, ptr, ptr, cint, ptr, ptr]
     lib.pi0x_sample_cache.restype = cint
+    if torch is not None:
+        from . import _binding
+        _binding.setup(torch, _fail)
+        _native = _binding
     _lib = lib
     return lib
 
@@ -204,77 +214,6 @@ def attention_noalloc(q, ks, vs, prefix_k, prefix_v, mask, B, H, P, step0, out, 
     return out
 
 
-def _device_of(what: str, *tensors) -> int:
-    """Index of the CUDA device that every given tensor (None: left out) lies on."""
-    index = None
-    for t in tensors:
-        if t is not None:
-            i = t.get_device()
-            if i != index:
-                if i < 0:
-                    raise ValueError(f"{what}: every tensor must be on a CUDA device")
-                if index is not None:
-                    raise ValueError(f"{what}: tensors on cuda:{index} and cuda:{i}")
-                index = i
-    return index
-
-
-def _row_type(what: str, t) -> int:
-    if t.dtype is torch.bfloat16:
-        return PI0X_DTYPE_BF16
-    if t.dtype is torch.float32:
-        return PI0X_DTYPE_F32
-    raise ValueError(f"{what}: rows are bfloat16 or float32, not {t.dtype}")
-
-
-def _rows(what: str, t, B: int, T: int, heads: int, D: int, dtype) -> Rows:
-    """(B, T, heads, D) tensor of `dtype` as strided rows."""
-    if t.shape != (B, T, heads, D) or t.dtype is not dtype:
-        raise ValueError(f"{what}: expected {(B, T, heads, D)} {dtype} rows, got {tuple(t.shape)} {t.dtype}")
-    sb, st, sh, one = t.stride()
-    if one != 1:
-        raise ValueError(f"{what}: rows need a contiguous last dimension")
-    return Rows(t.data_ptr(), sb, st, sh)
-
-
-def _new_rows(t):
-    """A new contiguous tensor like `t`, and its rows."""
-    B, T, heads, D = t.shape
-    out = torch.empty_like(t, memory_format=torch.contiguous_format)
-    return out, Rows(out.data_ptr(), T * heads * D, heads * D, D)
-
-
-def _ints(what: str, name: str, t, *shape):
-    if t is None:
-        return 0
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: {name} must be a contiguous int32 tensor of shape {shape}")
-    return t.data_ptr()
-
-
-def _mask(what: str, t, B: int):
-    """Pointer and length of a (B, length) mask (None: 0, 0)."""
-    if t is None:
-        return 0, 0
-    if (t.dtype is not torch.uint8 and t.dtype is not torch.bool) or t.dim() != 2 or t.shape[0] != B or \
-            t.shape[1] < 1 or not t.is_contiguous():
-        raise ValueError(f"{what}: mask must be a contiguous uint8 or bool tensor of shape ({B}, 1 or more)")
-    return t.data_ptr(), t.shape[1]
-
-
-def _gain(what: str, t, head_dim: int):
-    if t is None:
-        return 0
-    if t.dtype is not torch.float32 or t.shape != (head_dim,) or not t.is_contiguous():
-        raise ValueError(f"{what}: a gain is a contiguous float32 tensor of shape ({head_dim},)")
-    return t.data_ptr()
-
-
-def _current_stream(index: int) -> int:
-    """torch's current stream on device `index`, as a handle."""
-    return torch._C._cuda_getCurrentRawStream(index)
-
-
 def qk_norm_rope(q, k=None, start=None, *, positions=None, q_gain=None, k_gain=None, eps: float = 1e-6,
                  rope_base: Optional[float] = 10000.0, q_out=None, k_out=None):
     """Per-head RMSNorm (where a gain is given: gain 1 + g) and rotate-half rotation of
@@ -287,37 +226,13 @@ def qk_norm_rope(q, k=None, start=None, *, positions=None, q_gain=None, k_gain=N
     (q_out, k_out), new tensors unless given; an output may be its own input.
     Runs on the current stream of the tensors' device.
     """
-    what = "qk_norm_rope"
-    index = _device_of(what, q, k, start, positions, q_gain, k_gain, q_out, k_out)
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(index):
-            return qk_norm_rope(q, k, start, positions=positions, q_gain=q_gain, k_gain=k_gain, eps=eps,
-                                rope_base=rope_base, q_out=q_out, k_out=k_out)
-    dtype = _row_type(what, q)
-    if q.dim() != 4 or (k is not None and k.dim() != 4):
-        raise ValueError(f"{what}: q and k are (batch, tokens, heads, head_dim)")
-    B, T, heads, D = q.shape
-    kv = 0 if k is None else k.shape[2]
-    rq = _rows(what, q, B, T, heads, D, q.dtype)
-    rk = None if k is None else _rows(what, k, B, T, kv, D, q.dtype)
-    rot = Rotation(_gain(what, q_gain, D), _gain(what, k_gain, D), _ints(what, "positions", positions, B, T), eps,
-                   rope_base or 0.0)
-    first = _ints(what, "start", start, B)
-    if q_out is None:
-        q_out, rqo = _new_rows(q)
-    else:
-        rqo = _rows(what, q_out, B, T, heads, D, q.dtype)
-    rko = None
-    if k is not None:
-        if k_out is None:
-            k_out, rko = _new_rows(k)
-        else:
-            rko = _rows(what, k_out, B, T, kv, D, q.dtype)
-    if B * T * (heads + kv) == 0:
-        return q_out, k_out
-    _check(load().pi0x_qk_norm_rope(dtype, B, T, heads, kv, D, rq, rk, first, rot, rqo, rko, _current_stream(index)),
-           "pi0x_qk_norm_rope")
-    return q_out, k_out
+    if _native is None:
+        load()
+    r = _native.qk_norm_rope(q, k, start, positions, q_gain, k_gain, eps, rope_base, q_out, k_out)
+    if r is NotImplemented:
+        with torch.cuda.device(q.device):
+            return _native.qk_norm_rope(q, k, start, positions, q_gain, k_gain, eps, rope_base, q_out, k_out)
+    return r
 
 
 class KVCache:
@@ -343,13 +258,16 @@ class KVCache:
         for s in (k_scale, v_scale):
             if s is not None and (s.dtype != torch.float32 or s.shape != k.shape[:4] or not s.is_contiguous()):
                 raise ValueError("KVCache: scales must be contiguous float32 (layers, num_pages, page_size, kv_heads)")
-        self._index = _device_of("KVCache", k, v, k_scale, v_scale)
+        for t in (k, v, k_scale, v_scale):
+            if t is not None and (not t.is_cuda or t.device != k.device):
+                raise ValueError("KVCache: every pool must be on one CUDA device")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.layers, self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         self.device = k.device
+        self._index = k.device.index
         self._desc = Cache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), *k.shape, types[k.dtype])
-        self._lib = load()
-        self._attend_bytes = {}  # workspace bytes by (batch, heads, max_pages)
+        self._address = ctypes.addressof(self._desc)
+        load()
 
     @classmethod
     def empty(cls, layers: int, num_pages: int, page_size: int, kv_heads: int = 1, head_dim: int = 256,
@@ -364,18 +282,13 @@ class KVCache:
             pools += [torch.zeros(shape[:4], dtype=torch.float32, device=device) for _ in range(2)]
         return cls(*pools)
 
-    def _elsewhere(self, what: str, *tensors) -> bool:
-        """Checks that the tensors lie with the cache; True if another device is current."""
-        index = _device_of(what, *tensors)
-        if index != self._index:
-            raise ValueError(f"{what}: tensors on cuda:{index}, the cache on cuda:{self._index}")
-        return index != torch.cuda.current_device()
-
-    def _pages(self, what: str, table, B: int):
-        """Pointer and width of the page table of B samples."""
-        if table.dtype is not torch.int32 or table.dim() != 2 or table.shape[0] != B or not table.is_contiguous():
-            raise ValueError(f"{what}: table must be a contiguous int32 tensor of shape ({B}, max_pages)")
-        return table.data_ptr(), table.shape[1]
+    def _call(self, function, *args):
+        """`function` of the native binding on this cache, with its device current."""
+        r = function(self._address, self._index, *args)
+        if r is NotImplemented:
+            with torch.cuda.device(self._index):
+                return function(self._address, self._index, *args)
+        return r
 
     def write(self, layer: int, k, v, table, start, count=None, *, q=None, q_out=None, positions=None, q_gain=None,
               k_gain=None, eps: float = 1e-6, rope_base: Optional[float] = None):
@@ -387,37 +300,8 @@ class KVCache:
         :func:`qk_norm_rope`, and so is ``q`` (B, T, heads, head_dim), in the same pass.
         Returns ``q_out`` (new unless given), or None without q.
         """
-        what = "KVCache.write"
-        if self._elsewhere(what, k, v, table, start, count, q, q_out, positions, q_gain, k_gain):
-            with torch.cuda.device(self._index):
-                return self.write(layer, k, v, table, start, count, q=q, q_out=q_out, positions=positions,
-                                  q_gain=q_gain, k_gain=k_gain, eps=eps, rope_base=rope_base)
-        dtype = _row_type(what, k)
-        if k.dim() != 4 or (q is not None and q.dim() != 4):
-            raise ValueError(f"{what}: q, k and v are (batch, tokens, heads, head_dim)")
-        B, T = k.shape[:2]
-        D, kv = self.head_dim, self.kv_heads
-        rk, rv = _rows(what, k, B, T, kv, D, k.dtype), _rows(what, v, B, T, kv, D, k.dtype)
-        pages, max_pages = self._pages(what, table, B)
-        if start is None:
-            raise ValueError(f"{what}: start is required")
-        first, n = _ints(what, "start", start, B), _ints(what, "count", count, B)
-        rot = rq = rqo = None
-        heads = 0
-        if q is not None or rope_base or q_gain is not None or k_gain is not None:
-            rot = Rotation(_gain(what, q_gain, D), _gain(what, k_gain, D),
-                           _ints(what, "positions", positions, B, T), eps, rope_base or 0.0)
-        if q is not None:
-            heads = q.shape[2]
-            rq = _rows(what, q, B, T, heads, D, k.dtype)
-            if q_out is None:
-                q_out, rqo = _new_rows(q)
-            else:
-                rqo = _rows(what, q_out, B, T, heads, D, k.dtype)
-        if B * T:
-            _check(self._lib.pi0x_cache_write(self._desc, layer, dtype, B, T, rk, rv, pages, max_pages, first, n, rot,
-                                              heads, rq, rqo, _current_stream(self._index)), "pi0x_cache_write")
-        return q_out
+        return self._call(_native.cache_write, layer, k, v, table, start, count, q, q_out, positions, q_gain, k_gain,
+                          eps, rope_base)
 
     def read(self, table, lens, length: int, *, mask=None, layer0: int = 0, layers: Optional[int] = None, dtype=None,
              k_out=None, v_out=None, mask_out=None):
@@ -427,36 +311,9 @@ class KVCache:
         that hold a key: below ``lens[b]``, on a page of the pool and, with ``mask`` (B,
         length), nonzero there.  The others come out as zeros (pi0x_cache_read).
         """
-        what = "KVCache.read"
-        if self._elsewhere(what, table, lens, mask, k_out, v_out, mask_out):
-            with torch.cuda.device(self._index):
-                return self.read(table, lens, length, mask=mask, layer0=layer0, layers=layers, dtype=dtype,
-                                 k_out=k_out, v_out=v_out, mask_out=mask_out)
-        B = table.shape[0]
-        pages, max_pages = self._pages(what, table, B)
-        keys = _ints(what, "lens", lens, B)
         n = self.layers - layer0 if layers is None else layers
-        if n < 0 or length < 0:
-            raise ValueError(f"{what}: {n} layers of {length} slots")
-        dtype = dtype or torch.bfloat16
-        m, mask_len = _mask(what, mask, B)
-        if mask is not None and mask_len != length:
-            raise ValueError(f"{what}: mask covers {mask_len} slots, not {length}")
-        shape = (n, B, self.kv_heads, length, self.head_dim)
-        outs = []
-        for t, sh, dt in ((k_out, shape, dtype), (v_out, shape, dtype), (mask_out, (B, length), torch.uint8)):
-            if t is None:
-                t = torch.empty(sh, dtype=dt, device=self.device)
-            elif t.shape != sh or t.dtype != dt or not t.is_contiguous():
-                raise ValueError(f"{what}: outputs must be contiguous {shape} {dtype} and ({B}, {length}) uint8")
-            outs.append(t)
-        k_out, v_out, mask_out = outs
-        code = _row_type(what, k_out)
-        if B * length:
-            _check(self._lib.pi0x_cache_read(self._desc, layer0, n, B, length, pages, max_pages, keys, m, code,
-                                             k_out.data_ptr(), v_out.data_ptr(), mask_out.data_ptr(),
-                                             _current_stream(self._index)), "pi0x_cache_read")
-        return k_out, v_out, mask_out
+        return self._call(_native.cache_read, table, lens, length, mask, layer0, n, dtype or torch.bfloat16, k_out,
+                          v_out, mask_out)
 
     def attend(self, layer: int, q, table, lens, *, mask=None, scale: Optional[float] = None, out=None, lse=None):
         """Attention of one new token a sample over the pages of ``layer``
@@ -466,40 +323,8 @@ class KVCache:
         head_dim ** -0.5.  Returns (out, lse): (B, heads, head_dim) bf16 and (B, heads)
         fp32, zeros and -inf for a sample without keys.
         """
-        what = "KVCache.attend"
-        if self._elsewhere(what, q, table, lens, mask, out, lse):
-            with torch.cuda.device(self._index):
-                return self.attend(layer, q, table, lens, mask=mask, scale=scale, out=out, lse=lse)
-        D = self.head_dim
-        if q.dim() != 3 or q.dtype is not torch.bfloat16 or q.shape[2] != D or q.stride(2) != 1:
-            raise ValueError(f"{what}: q must be (batch, heads, {D}) bfloat16 with a contiguous last dimension")
-        B, heads, _ = q.shape
-        pages, max_pages = self._pages(what, table, B)
-        keys = _ints(what, "lens", lens, B)
-        m, mask_len = _mask(what, mask, B)
-        if out is None:
-            out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        elif out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous():
-            raise ValueError(f"{what}: out must be contiguous and like q")
-        if lse is None:
-            lse = torch.empty((B, heads), dtype=torch.float32, device=self.device)
-        elif lse.shape != (B, heads) or lse.dtype is not torch.float32 or not lse.is_contiguous():
-            raise ValueError(f"{what}: lse must be contiguous float32 ({B}, {heads})")
-        if B * heads == 0:
-            return out, lse
-        need = self._attend_bytes.get((B, heads, max_pages))
-        if need is None:
-            need = self._lib.pi0x_cache_attention_workspace(self._desc, B, heads, max_pages)
-            if len(self._attend_bytes) < 4096:
-                self._attend_bytes[B, heads, max_pages] = need
-        # a workspace of this call alone, from torch's allocator on the current stream
-        work = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-        sb, sh, _ = q.stride()
-        _check(self._lib.pi0x_cache_attention(
-            self._desc, layer, B, heads, Rows(q.data_ptr(), sb, 0, sh), pages, max_pages, keys, m, mask_len,
-            D ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(), work.data_ptr() if need else 0,
-            need, _current_stream(self._index)), "pi0x_cache_attention")
-        return out, lse
+        return self._call(_native.cache_attention, layer, q, table, lens, mask,
+                          self.head_dim ** -0.5 if scale is None else scale, out, lse)
 
 
 class Sampler:
@@ -575,20 +400,20 @@ class Sampler:
         """Enqueue one call whose prefix K/V are slots 0..length-1 of a paged cache, as
         :meth:`KVCache.read` reads them (pi0x_sample_cache).  Runs on the current stream
         of the cache's device."""
-        what = "Sampler.sample_cache"
-        if cache._elsewhere(what, table, lens, mask):
-            with torch.cuda.device(cache._index):
-                return self.sample_cache(cache, table, lens, length, state, x1, num_steps, mask=mask, x0=x0)
+        B = int(table.shape[0])
+        for name, t, dtypes, shape in (("table", table, (torch.int32,), (B, table.shape[-1])),
+                                       ("lens", lens, (torch.int32,), (B,)),
+                                       ("mask", mask, (torch.uint8, torch.bool), (B, length))):
+            if t is not None and (t.device != cache.device or t.dtype not in dtypes or t.shape != shape or
+                                  not t.is_contiguous()):
+                raise ValueError(f"Sampler.sample_cache: {name} must be a contiguous {dtypes[0]} tensor of shape "
+                                 f"{tuple(shape)} on {cache.device}")
         if x0 is None:
             x0 = x1.new_empty(x1.shape) if hasattr(x1, "new_empty") else np.empty_like(x1)
-        B = int(table.shape[0])
-        pages, max_pages = cache._pages(what, table, B)
-        m, mask_len = _mask(what, mask, B)
-        if mask is not None and mask_len != length:
-            raise ValueError(f"{what}: mask covers {mask_len} slots, not {length}")
-        _check(self._lib.pi0x_sample_cache(self._h, cache._desc, B, length, pages, max_pages,
-                                           _ints(what, "lens", lens, B), m, _ptr(state), _ptr(x1), int(num_steps),
-                                           _ptr(x0), _current_stream(cache._index)), "pi0x_sample_cache")
+        with torch.cuda.device(cache.device):
+            _check(self._lib.pi0x_sample_cache(
+                self._h, cache._desc, B, length, _ptr(table), int(table.shape[1]), _ptr(lens), _ptr(mask), _ptr(state),
+                _ptr(x1), int(num_steps), _ptr(x0), torch.cuda.current_stream().cuda_stream), "pi0x_sample_cache")
         return x0
 
     def set_variant(self, time_grid: int = PI0X_TIME_PI0, x_prediction: bool = False,
