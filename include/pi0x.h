@@ -135,13 +135,15 @@ int pi0x_sample(pi0x_handle *h, const void *const *prefix_k, const void *const *
 int pi0x_sync_status(pi0x_handle *h);
 
 /* ---- paged prefix cache --------------------------------------------------------
+ * For inference, as the rest of the library: no call has a backward pass.
  * pi0x_sample takes the prefix keys and values as contiguous bf16 tensors.  The
  * calls below make and hold them: per-head norm and rotation of queries and keys
  * (pi0x_qk_norm_rope), a cache in pages shared by many samples, in bf16 or 8 bits
  * (pi0x_cache_write, pi0x_cache_read), attention of one new token a sample over it
  * (pi0x_cache_attention) and the denoising loop on it (pi0x_sample_cache).
  *
- * Every pointer below is device memory of the current device.  The calls enqueue
+ * Every pointer below is device memory of the current device, of its elements'
+ * alignment at least.  The calls enqueue
  * their work on `stream` and return; they allocate nothing, keep nothing, and may be
  * captured into a CUDA graph (pi0x_sample_cache excepted).  What can be seen from the host is checked
  * (PI0X_EINVAL, PI0X_EUNSUPPORTED); what lies in device memory is bounded by the
@@ -174,7 +176,7 @@ typedef struct {
  * more).  The angle is exact to 2^-32 of a turn at every 32-bit position; all of it
  * is fp32, rounded once to the output's type. */
 typedef struct {
-  const float *q_gain, *k_gain;  /* (head_dim) fp32, 16-byte aligned; NULL: no norm */
+  const float *q_gain, *k_gain;  /* (head_dim) fp32; NULL: no norm */
   const int32_t *positions;      /* (B, T); NULL: start[b] + t */
   float eps;                     /* > 0 where a gain is given */
   float rope_base;               /* 0: no rotation */

@@ -56,7 +56,8 @@ def test_bad_caches_are_refused_by_every_call(lib, kw, status):
     (dict(pages=1 << 27), EINVAL), (dict(start=None), EINVAL), (dict(heads=8), EINVAL),
     (dict(heads=8, rot=Rotation(0, 0, 0, 1e-6, 1e4)), EINVAL), (dict(heads=-1), EINVAL),
     (dict(rot=Rotation(0, PTR, 0, 0.0, 1e4)), EINVAL), (dict(rot=Rotation(0, 0, 0, 1e-6, 0.5)), EINVAL),
-    (dict(rot=Rotation(0, 0, 0, 1e-6, float("nan"))), EINVAL), (dict(rot=Rotation(0, PTR + 4, 0, 1e-6, 1e4)), EINVAL),
+    (dict(rot=Rotation(0, 0, 0, 1e-6, float("nan"))), EINVAL), (dict(rot=Rotation(0, PTR + 2, 0, 1e-6, 1e4)), EINVAL),
+    (dict(rot=Rotation(0, 0, PTR + 1, 1e-6, 1e4)), EINVAL), (dict(start=PTR + 2), EINVAL), (dict(table=PTR + 2), EINVAL),
     (dict(B=1 << 16, T=1 << 14), EINVAL),
 ], ids=str)
 def test_cache_write_refuses(lib, kw, status):
@@ -68,7 +69,7 @@ def test_cache_write_refuses(lib, kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(layer0=1, layers=2), EINVAL), (dict(layers=0), EINVAL), (dict(P=0), EINVAL), (dict(lens=None), EINVAL),
-    (dict(k=None), EINVAL), (dict(k=PTR + 8), EINVAL), (dict(dtype=INT8), EUNSUP), (dict(B=1 << 16, P=1 << 15), EINVAL),
+    (dict(lens=PTR + 3), EINVAL), (dict(k=None), EINVAL), (dict(k=PTR + 8), EINVAL), (dict(dtype=INT8), EUNSUP), (dict(B=1 << 16, P=1 << 15), EINVAL),
 ], ids=str)
 def test_cache_read_refuses(lib, kw, status):
     d = dict(layer0=0, layers=1, B=1, P=8, lens=PTR, dtype=BF16, k=PTR)
@@ -81,7 +82,8 @@ def test_cache_read_refuses(lib, kw, status):
     (dict(layer=2), EINVAL), (dict(heads=0), EINVAL), (dict(heads=7), EINVAL), (dict(lens=None), EINVAL),
     (dict(out=None), EINVAL), (dict(out=PTR + 2), EINVAL), (dict(q=None), EINVAL), (dict(q=rows(PTR + 2)), EINVAL),
     (dict(mask=PTR, mask_len=0), EINVAL), (dict(scale=float("inf")), EINVAL), (dict(scale=float("nan")), EINVAL),
-    (dict(B=65536), EINVAL), (dict(heads=65536), EINVAL),
+    (dict(B=65536), EINVAL), (dict(heads=65536), EINVAL), (dict(B=60000, heads=60000), EINVAL),
+    (dict(scale=3e38), EINVAL), (dict(lens=PTR + 1), EINVAL),
 ], ids=str)
 def test_cache_attention_refuses(lib, kw, status):
     d = dict(layer=0, B=1, heads=8, q=rows(), lens=PTR, mask=None, mask_len=0, scale=0.1, out=PTR)

@@ -180,6 +180,58 @@ def test_empty_batches_return_empty():
     assert c.read(table, none, 5)[0].shape == (1, 0, 1, 5, 64)
 
 
+def test_python_refusals_on_the_gpu():
+    g = rng(3)
+    c = pi0x.KVCache.empty(2, 8, 4, 2, 64, "bf16")
+    q, k = randn(g, 2, 3, 4, 64, dtype=BF16), randn(g, 2, 3, 2, 64, dtype=BF16)
+    table, lens = ints([[0, 1], [2, 3]]), ints([1, 2])
+    bad = [
+        (ValueError, lambda: pi0x.qk_norm_rope(q, k.float(), lens)),
+        (ValueError, lambda: pi0x.qk_norm_rope(q.half())),
+        (ValueError, lambda: pi0x.qk_norm_rope(q[0])),
+        (ValueError, lambda: pi0x.qk_norm_rope(q, k[:, :2])),
+        (ValueError, lambda: pi0x.qk_norm_rope(q.transpose(2, 3))),
+        (ValueError, lambda: pi0x.qk_norm_rope(q, k, lens.long())),
+        (ValueError, lambda: pi0x.qk_norm_rope(q, k, ints([1, 2, 3]))),
+        (ValueError, lambda: pi0x.qk_norm_rope(q, k, positions=lens)),
+        (ValueError, lambda: pi0x.qk_norm_rope(q, k, q_gain=torch.zeros(32, device="cuda"))),
+        (ValueError, lambda: pi0x.qk_norm_rope(q, k, q_out=torch.empty_like(k))),
+        (ValueError, lambda: pi0x.qk_norm_rope(q, k.cpu(), lens)),
+        (pi0x.Pi0xError, lambda: pi0x.qk_norm_rope(q[..., :32].contiguous())),
+        (pi0x.Pi0xError, lambda: pi0x.qk_norm_rope(q, rope_base=0.25)),
+        (pi0x.Pi0xError, lambda: pi0x.qk_norm_rope(randn(g, 2, 3, 4, 65, dtype=BF16)[..., :64])),
+        (ValueError, lambda: c.write(0, q, q, table, lens)),
+        (ValueError, lambda: c.write(0, k, k[:, :1], table, lens)),
+        (ValueError, lambda: c.write(0, k, k, table[:1], lens)),
+        (ValueError, lambda: c.write(0, k, k, table.T, lens)),
+        (ValueError, lambda: c.write(0, k, k, table, None)),
+        (ValueError, lambda: c.write(0, k, k, table, lens, q=q.float())),
+        (pi0x.Pi0xError, lambda: c.write(2, k, k, table, lens)),
+        (pi0x.Pi0xError, lambda: c.write(-1, k, k, table, lens)),
+        (ValueError, lambda: c.read(table, ints([1]), 3)),
+        (ValueError, lambda: c.read(table, lens, 3, mask=torch.ones(2, 4, device="cuda", dtype=torch.uint8))),
+        (ValueError, lambda: c.read(table, lens, 3, dtype=torch.float16)),
+        (ValueError, lambda: c.read(table, lens, -3)),
+        (ValueError, lambda: c.read(table, lens, 3, k_out=torch.empty(2, 2, 3, 2, 64, device="cuda", dtype=BF16))),
+        (pi0x.Pi0xError, lambda: c.read(table, lens, 3, layer0=1, layers=2)),
+        (ValueError, lambda: c.attend(0, q, table, lens)),
+        (ValueError, lambda: c.attend(0, q[:, 0].float(), table, lens)),
+        (ValueError, lambda: c.attend(0, q[:, 0], table, None)),
+        (ValueError, lambda: c.attend(0, q[:, 0], table, lens, mask=torch.ones(2, 0, device="cuda", dtype=torch.uint8))),
+        (ValueError, lambda: c.attend(0, q[:, 0], table, lens, lse=torch.empty(2, 3, device="cuda"))),
+        (pi0x.Pi0xError, lambda: c.attend(0, q[:, 0, :3], table, lens)),
+        (pi0x.Pi0xError, lambda: c.attend(5, q[:, 0], table, lens)),
+        (pi0x.Pi0xError, lambda: c.attend(0, q[:, 0], table, lens, scale=float("nan"))),
+        (OverflowError, lambda: c.attend(2 ** 40, q[:, 0], table, lens)),
+        (AttributeError, lambda: c.attend(0, [1.0], table, lens)),
+    ]
+    for i, (error, call) in enumerate(bad):
+        with pytest.raises(error):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    torch.cuda.synchronize()
+
+
 # ---- writing and reading pages -----------------------------------------------------
 
 

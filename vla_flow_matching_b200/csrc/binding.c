@@ -171,10 +171,12 @@ static int take_table(const char *what, PyObject *t, int64_t *B, const int32_t *
 }
 
 /* (B, length) uint8 or bool mask, or None (NULL, 0). */
-static int take_mask(const char *what, PyObject *t, int64_t B, const uint8_t **p, int64_t *length, long *device) {
+static int take_mask(const char *what, PyObject *t, int64_t B, const uint8_t **p, int64_t *length, PyObject **dtype,
+                     long *device) {
   View v;
   *p = NULL;
   *length = 0;
+  *dtype = NULL;
   if (t == Py_None) return 0;
   if (take(what, t, &v, device)) return -1;
   if ((v.dtype != t_u8 && v.dtype != t_bool) || v.ndim != 2 || v.shape[0] != B || v.shape[1] < 1 ||
@@ -185,6 +187,7 @@ static int take_mask(const char *what, PyObject *t, int64_t B, const uint8_t **p
   }
   *p = (const uint8_t *)v.data;
   *length = v.shape[1];
+  *dtype = v.dtype;
   return 0;
 }
 
@@ -432,6 +435,7 @@ static PyObject *py_cache_read(PyObject *self, PyObject *const *a, Py_ssize_t n)
   int64_t B = -1, mask_len;
   const int32_t *table, *lens;
   const uint8_t *mask;
+  PyObject *mask_type;
   int max_pages;
   const int dtype = row_type(what, a[8]);
   if (dtype < 0) return NULL;
@@ -440,7 +444,7 @@ static PyObject *py_cache_read(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return NULL;
   }
   if (take_table(what, a[2], &B, &table, &max_pages, &device) || fits(what, B, 0, 0) ||
-      take_ints(what, "lens", a[3], 1, &B, &lens, &device) || take_mask(what, a[5], B, &mask, &mask_len, &device))
+      take_ints(what, "lens", a[3], 1, &B, &lens, &device) || take_mask(what, a[5], B, &mask, &mask_len, &mask_type, &device))
     return NULL;
   if (a[3] == Py_None || (mask && mask_len != length)) {
     PyErr_Format(PyExc_ValueError, "%s: lens is required, and a mask covers the %d slots read", what, length);
@@ -452,7 +456,8 @@ static PyObject *py_cache_read(PyObject *self, PyObject *const *a, Py_ssize_t n)
   void *pk, *pv, *pm;
   PyObject *k = out_tensor(what, "k_out", a[9], NULL, 5, shape, a[8], &device, &pk), *r = NULL;
   PyObject *v = k ? out_tensor(what, "v_out", a[10], k, 5, shape, a[8], &device, &pv) : NULL;
-  PyObject *m = v ? out_tensor(what, "mask_out", a[11], NULL, 2, mshape, t_u8, &device, &pm) : NULL;
+  PyObject *like = mask && mask_type == t_u8 ? a[5] : NULL;
+  PyObject *m = v ? out_tensor(what, "mask_out", a[11], like, 2, mshape, t_u8, &device, &pm) : NULL;
   if (!m) goto out;
   if (B * length != 0) {
     void *stream;
@@ -485,6 +490,7 @@ static PyObject *py_cache_attention(PyObject *self, PyObject *const *a, Py_ssize
   View q;
   const int32_t *table, *lens;
   const uint8_t *mask;
+  PyObject *mask_type;
   int64_t mask_len;
   int max_pages;
   if (take(what, a[3], &q, &device)) return NULL;
@@ -496,7 +502,7 @@ static PyObject *py_cache_attention(PyObject *self, PyObject *const *a, Py_ssize
   int64_t B = q.shape[0];
   const int64_t heads = q.shape[1];
   if (fits(what, B, heads, 0) || take_table(what, a[4], &B, &table, &max_pages, &device) ||
-      take_ints(what, "lens", a[5], 1, &B, &lens, &device) || take_mask(what, a[6], B, &mask, &mask_len, &device))
+      take_ints(what, "lens", a[5], 1, &B, &lens, &device) || take_mask(what, a[6], B, &mask, &mask_len, &mask_type, &device))
     return NULL;
   if (a[5] == Py_None) {
     PyErr_Format(PyExc_ValueError, "%s: lens is required", what);

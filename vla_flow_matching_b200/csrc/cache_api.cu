@@ -24,6 +24,7 @@ int launched(cudaError_t e, const char *what) {
   return e == cudaErrorMemoryAllocation ? PI0X_ENOMEM : PI0X_ECUDA;
 }
 bool aligned(const void *p, size_t n = 16) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+constexpr float kLog2e = 1.4426950408889634f;
 bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
 
 // Rows of `elem`-byte elements: data and strides in whole 16 bytes.
@@ -36,7 +37,7 @@ RowsPtr rows_of(const pi0x_rows *r) { return RowsPtr{r->data, r->batch_stride, r
 
 bool rotation_ok(const pi0x_rotation *r) {
   const bool gains = r->q_gain || r->k_gain;
-  return aligned(r->q_gain) && aligned(r->k_gain) && (!gains || (r->eps > 0.0f && isfinite(r->eps))) &&
+  return aligned(r->q_gain, 4) && aligned(r->k_gain, 4) && aligned(r->positions, 4) && (!gains || (r->eps > 0.0f && isfinite(r->eps))) &&
          (r->rope_base == 0.0f || (r->rope_base >= 1.0f && isfinite(r->rope_base)));
 }
 
@@ -56,10 +57,10 @@ void set_turns(RowArgs &a, float base, int head_dim) {
   for (int i = 0; i < head_dim / 2; ++i) a.turn[i] = turn[i];
 }
 
-// q, k and the rotation of a RowArgs; false if something does not fit.
+// The norms and the rotation of a RowArgs whose heads are set.
 void set_rotation(RowArgs &a, const pi0x_rotation *rot, int head_dim) {
   a.q_gain = a.hq ? rot->q_gain : nullptr;
-  a.k_gain = rot->k_gain;
+  a.k_gain = a.hk ? rot->k_gain : nullptr;
   a.eps = rot->eps;
   a.positions = rot->positions;
   a.rotate = rot->rope_base > 0.0f;
@@ -69,9 +70,9 @@ void set_rotation(RowArgs &a, const pi0x_rotation *rot, int head_dim) {
 }  // namespace
 
 int check_cache(const pi0x_cache *c, int layer0, int layers, int B, const int32_t *table, int max_pages) {
-  if (!c || !c->k || !c->v || !table || B < 1 || max_pages < 1 || c->layers < 1 || c->num_pages < 1 ||
+  if (!c || !c->k || !c->v || !table || !aligned(table, 4) || B < 1 || max_pages < 1 || c->layers < 1 || c->num_pages < 1 ||
       c->page_size < 1 || c->kv_heads < 1 || layer0 < 0 || layers < 1 || layers > c->layers - layer0)
-    return refuse(PI0X_EINVAL, "paged cache: null pointer, size below 1 or layer out of range");
+    return refuse(PI0X_EINVAL, "paged cache: null or misaligned pointer, size below 1 or layer out of range");
   if (c->dtype != PI0X_DTYPE_BF16 && c->dtype != PI0X_DTYPE_E4M3 && c->dtype != PI0X_DTYPE_INT8)
     return refuse(PI0X_EUNSUPPORTED, "paged cache: pages are bf16, e4m3 or int8");
   if (!head_dim_ok(c->head_dim)) return refuse(PI0X_EUNSUPPORTED, "paged cache: head_dim is 64, 128 or 256");
@@ -105,8 +106,8 @@ extern "C" {
 int pi0x_qk_norm_rope(int dtype, int B, int T, int q_heads, int k_heads, int head_dim, const pi0x_rows *q,
                       const pi0x_rows *k, const int32_t *start, const pi0x_rotation *rot, const pi0x_rows *q_out,
                       const pi0x_rows *k_out, void *stream) {
-  if (!rot || B < 1 || T < 1 || q_heads < 0 || k_heads < 0 || (q_heads == 0 && k_heads == 0))
-    return refuse(PI0X_EINVAL, "pi0x_qk_norm_rope: null rotation, size below 1 or no heads");
+  if (!rot || !aligned(start, 4) || B < 1 || T < 1 || q_heads < 0 || k_heads < 0 || (q_heads == 0 && k_heads == 0))
+    return refuse(PI0X_EINVAL, "pi0x_qk_norm_rope: null rotation, misaligned start, size below 1 or no heads");
   if (dtype != PI0X_DTYPE_BF16 && dtype != PI0X_DTYPE_F32)
     return refuse(PI0X_EUNSUPPORTED, "pi0x_qk_norm_rope: rows are bf16 or f32");
   if (!head_dim_ok(head_dim)) return refuse(PI0X_EUNSUPPORTED, "pi0x_qk_norm_rope: head_dim is 64, 128 or 256");
@@ -126,7 +127,6 @@ int pi0x_qk_norm_rope(int dtype, int B, int T, int q_heads, int k_heads, int hea
   if (k_heads) a.k = rows_of(k), a.k_out = rows_of(k_out);
   a.start = start;
   set_rotation(a, rot, head_dim);
-  if (!k_heads) a.k_gain = nullptr;
   return launched(launch_rows(a, dtype, PI0X_DTYPE_BF16, head_dim, (cudaStream_t)stream), "pi0x_qk_norm_rope");
 }
 
@@ -136,8 +136,8 @@ int pi0x_cache_write(const pi0x_cache *cache, int layer, int dtype, int B, int T
                      const pi0x_rows *q_out, void *stream) {
   const int st = check_cache(cache, layer, 1, B, table, max_pages);
   if (st) return st;
-  if (T < 1 || !start || q_heads < 0 || (q_heads && !rot))
-    return refuse(PI0X_EINVAL, "pi0x_cache_write: T below 1, no start, or q without a rotation");
+  if (T < 1 || !start || !aligned(start, 4) || !aligned(count, 4) || q_heads < 0 || (q_heads && !rot))
+    return refuse(PI0X_EINVAL, "pi0x_cache_write: T below 1, start missing, start or count misaligned, or q without a rotation");
   if (dtype != PI0X_DTYPE_BF16 && dtype != PI0X_DTYPE_F32)
     return refuse(PI0X_EUNSUPPORTED, "pi0x_cache_write: rows are bf16 or f32");
   const int elem = dtype == PI0X_DTYPE_F32 ? 4 : 2;
@@ -169,8 +169,8 @@ int pi0x_cache_read(const pi0x_cache *cache, int layer0, int layers, int B, int 
                     uint8_t *mask_out, void *stream) {
   const int st = check_cache(cache, layer0, layers, B, table, max_pages);
   if (st) return st;
-  if (P < 1 || !lens || !k_out || !v_out || !aligned(k_out) || !aligned(v_out))
-    return refuse(PI0X_EINVAL, "pi0x_cache_read: P below 1, a null pointer or an output off 16 bytes");
+  if (P < 1 || !lens || !aligned(lens, 4) || !k_out || !v_out || !aligned(k_out) || !aligned(v_out))
+    return refuse(PI0X_EINVAL, "pi0x_cache_read: P below 1, a null or misaligned pointer");
   if (dtype != PI0X_DTYPE_BF16 && dtype != PI0X_DTYPE_F32)
     return refuse(PI0X_EUNSUPPORTED, "pi0x_cache_read: outputs are bf16 or f32");
   if ((int64_t)B * P > INT32_MAX / layers / cache->kv_heads)
@@ -203,12 +203,13 @@ int pi0x_cache_attention(const pi0x_cache *cache, int layer, int B, int q_heads,
                          float scale, void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
   const int st = check_cache(cache, layer, 1, B, table, max_pages);
   if (st) return st;
-  if (q_heads < 1 || q_heads % cache->kv_heads || !lens || !out || !aligned(out) || !rows_ok(q, 2) ||
-      (mask && mask_len < 1) || !isfinite(scale))
+  if (q_heads < 1 || q_heads % cache->kv_heads || !lens || !aligned(lens, 4) || !out || !aligned(out) ||
+      !aligned(lse, 4) || !rows_ok(q, 2) || (mask && mask_len < 1) || !isfinite(scale * kLog2e))
     return refuse(PI0X_EINVAL,
                   "pi0x_cache_attention: heads that kv_heads does not divide, a null or misaligned pointer, an empty "
-                  "mask or a scale that is not finite");
-  if (B > 65535 || q_heads > 65535) return refuse(PI0X_EINVAL, "pi0x_cache_attention: over 65535 samples or heads");
+                  "mask or a scale that is not finite or beyond 2e38");
+  if (B > 65535 || q_heads > 65535 || (int64_t)B * q_heads > INT32_MAX)
+    return refuse(PI0X_EINVAL, "pi0x_cache_attention: over 65535 samples or heads, or 2^31 rows or more");
   const size_t need =
       attend_workspace(B, q_heads, cache->kv_heads, cache->head_dim, cache->dtype, cache->page_size, max_pages);
   if (need && (!workspace || !aligned(workspace) || workspace_bytes < need))
@@ -226,7 +227,7 @@ int pi0x_cache_attention(const pi0x_cache *cache, int layer, int B, int q_heads,
   a.lens = lens;
   a.mask = mask;
   a.mask_len = mask_len;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = scale * kLog2e;
   a.out = (bf16 *)out;
   a.lse = lse;
   a.part = (float *)workspace;

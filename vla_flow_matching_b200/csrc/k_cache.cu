@@ -159,10 +159,12 @@ __device__ __forceinline__ void turn_cos_sin_approx(uint32_t turn, float &c, flo
 
 // A lane holds 16 bytes of each half of a row, the pairs (i, i + D/2), so the rotation needs
 // no exchange; D/16 (bf16) or D/8 (fp32) lanes hold a row.  RowMath has what is done to a row.
-template <typename T, int D>
+// kExact: sines and cosines to fp32 (fp32 rows, and 8-bit codes, where an error next to the
+// border of two codes becomes a step between them).
+template <typename T, int D, bool kExact>
 struct RowMath {
   static constexpr int kN = Vec<T>::kN, kP = kN / 2, kLanes = D / 2 / kN;
-  f32x2 c[kP], s[kP];  // cosines and sines of the lane's pairs
+  f32x2 c[kP], s[kP], ns[kP];  // cosines, sines and their negatives of the lane's pairs
 
   // The tables in shared memory are laid out so that the lanes of a group read consecutive
   // words: entry i of lane l is turn i * kLanes + l; gains go four at a time.
@@ -180,20 +182,20 @@ struct RowMath {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t t = (uint32_t)(((uint64_t)pos * table[(2 * i + k) * kLanes] + 0x80000000u) >> 32);
-        if constexpr (sizeof(T) == 2)
-          turn_cos_sin_approx(t, cs[k], sn[k]);
-        else
+        if constexpr (kExact)
           turn_cos_sin(t, cs[k], sn[k]);
+        else
+          turn_cos_sin_approx(t, cs[k], sn[k]);
       }
       c[i] = pair(cs[0], cs[1]);
       s[i] = pair(sn[0], sn[1]);
+      ns[i] = pair(-sn[0], -sn[1]);
     }
   }
   __device__ __forceinline__ void rotate(f32x2 (&x)[kP], f32x2 (&y)[kP]) const {
-    const f32x2 minus = pair(-1.0f, -1.0f);
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
-      const f32x2 v = fma2(mul2(y[i], s[i]), minus, mul2(x[i], c[i]));
+      const f32x2 v = fma2(y[i], ns[i], mul2(x[i], c[i]));
       y[i] = fma2(y[i], c[i], mul2(x[i], s[i]));
       x[i] = v;
     }
@@ -238,7 +240,7 @@ struct RowMath {
 // 9 rows of 512 bytes each, move 241 MB.
 template <typename T, typename Pool, int D>
 __global__ void __launch_bounds__(256, 3) k_rows(const __grid_constant__ RowArgs a) {
-  using M = RowMath<T, D>;
+  using M = RowMath<T, D, sizeof(T) == 4 || Pool::kScaled>;
   constexpr int kN = M::kN, kP = M::kP, kLanes = M::kLanes, kGroups = 256 / kLanes, kAhead = 3;
   __shared__ uint64_t sm_turn[D / 2];  // lanes index it apart: from the parameters that would be one after another
   __shared__ __align__(16) float sm_gain[D];  // 1 + gain
@@ -437,7 +439,7 @@ namespace {
 
 template <typename T, typename Pool, int D>
 cudaError_t rows_go(RowArgs a, cudaStream_t s) {
-  constexpr uint32_t kGroups = 256 / RowMath<T, D>::kLanes;
+  constexpr uint32_t kGroups = 256 / RowMath<T, D, true>::kLanes;
   const uint32_t tokens = (uint32_t)a.B * a.T;
   // Heads of an item: all of a token's (up to 16) where there are enough tokens for two
   // blocks an SM, one where there are few.

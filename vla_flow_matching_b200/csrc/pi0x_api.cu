@@ -1160,8 +1160,14 @@ int pi0x_sample_cache(pi0x_handle *h, const pi0x_cache *cache, int B, int P, con
   if (!h || !lens || !state || !x1 || !x0 || B < 1 || B > 4096 || P < 1 || P > 8192 || num_steps < 1 ||
       num_steps > 1024)
     return PI0X_EINVAL;
-  int st = check_cache(cache, 0, h->cfg.depth, B, page_tab, max_pages);
+  int st = check_cache(cache, 0, 1, B, page_tab, max_pages);
   if (st) return st;
+  int dev = -1;
+  CK(cudaGetDevice(&dev));
+  if (dev != h->device || ((uintptr_t)lens & 3)) {
+    g_last_error = "pi0x_sample_cache: another device than the handle's is current, or lens is misaligned";
+    return PI0X_EINVAL;
+  }
   if (cache->layers != h->cfg.depth || cache->kv_heads != 1 || cache->head_dim != kHeadDim) {
     g_last_error = "pi0x_sample_cache: the cache must have the handle's depth, one kv head and head_dim 256";
     return PI0X_EINVAL;
