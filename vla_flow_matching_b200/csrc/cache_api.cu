@@ -210,6 +210,8 @@ int pi0x_cache_attention(const pi0x_cache *cache, int layer, int B, int q_heads,
                   "mask or a scale that is not finite or beyond 2e38");
   if (B > 65535 || q_heads > 65535 || (int64_t)B * q_heads > INT32_MAX)
     return refuse(PI0X_EINVAL, "pi0x_cache_attention: over 65535 samples or heads, or 2^31 rows or more");
+  if ((int64_t)B > INT32_MAX / (((int64_t)max_pages * cache->page_size + 63) / 64))
+    return refuse(PI0X_EINVAL, "pi0x_cache_attention: 2^31 blocks of 64 slots or more");
   const size_t need =
       attend_workspace(B, q_heads, cache->kv_heads, cache->head_dim, cache->dtype, cache->page_size, max_pages);
   if (need && (!workspace || !aligned(workspace) || workspace_bytes < need))

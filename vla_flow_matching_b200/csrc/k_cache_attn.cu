@@ -30,7 +30,6 @@ namespace pi0x {
 namespace {
 constexpr int kWarps = 4;
 constexpr int kHeadsPerUnit = 8;  // query heads of one kv head that share a pass: the product's columns
-constexpr int kMaxGrid = 148 * 3;
 constexpr int kJoinThreads = 512;
 constexpr float kWeightBits = 15.0f;
 constexpr int kMaxCluster = 8, kClusterBlocks = 8;
@@ -65,9 +64,9 @@ __device__ __forceinline__ uint32_t at_peer(const void *p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_u32(p)), "r"(rank));
   return d;
 }
-__device__ __forceinline__ float peer_load(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float2 peer_load2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ float4 peer_load4(uint32_t addr) {
@@ -178,6 +177,10 @@ struct __align__(16) Split {
   int first, last;  // its CTAs
   int slot;         // the first CTA's part; that of CTA c > first is 2c
 };
+// n / d, in 32 bits where n fits (a 64-bit division takes several times as long).
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d) {
+  return (uint64_t)n < (1ull << 32) && (uint64_t)d < (1ull << 32) ? (int64_t)((uint32_t)n / (uint32_t)d) : n / d;
+}
 template <int N>
 struct Look {
   int page[N];
@@ -211,16 +214,16 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
   extern __shared__ __align__(16) uint8_t sm_ring[];
   __shared__ __align__(16) uint8_t sm_q[kHeadsPerUnit][D * 2 + 16];
   __shared__ float sm_m[kWarps][kHeadsPerUnit], sm_l[kWarps][kHeadsPerUnit], sm_qf[kHeadsPerUnit];
-  __shared__ float sm_ml[2][kHeadsPerUnit];  // kCluster: this CTA's m and l
-  __shared__ int64_t sm_scan[kWarps], sm_at;
-  __shared__ int sm_b;
+  __shared__ float2 sm_ml[kHeadsPerUnit];  // kCluster: this CTA's m and l
+  __shared__ int64_t sm_at;
+  __shared__ int sm_scan[kWarps], sm_b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int group = a.heads / a.kv, groups = head_groups(a.heads, a.kv), upb = a.kv * groups;
   auto blocks_of = [](int len) { return max(1, (int)(((uint32_t)len + S::kBlock - 1) / S::kBlock)); };
 
   // ---- this CTA's blocks [c0, c1), its first sample, and where in the sample's units it starts
   int b;
-  int64_t c0, c1, at, total = 1, ctas = 1;
+  int64_t c0, c1, at, share = 1, longer = 0;  // a CTA's blocks; the first `longer` CTAs have one more
   Split *splits = reinterpret_cast<Split *>(a.part);
   float *parts = a.part + gridDim.x * (sizeof(Split) / 4);
   const bool by_unit = (int64_t)a.B * upb <= gridDim.x;
@@ -229,44 +232,57 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
     b = blockIdx.x / cluster / upb;
     c0 = c1 = at = 0;
   } else {
-    const int per = (a.B + kWarps * 32 - 1) / (kWarps * 32), b_lo = min(a.B, tid * per), b_hi = min(a.B, b_lo + per);
-    int64_t mine = 0;
+    // Up to 256 samples are counted by every warp on its own, more by the block.
+    const bool alone = a.B <= 256;
+    const int counters = alone ? 32 : kWarps * 32, id = alone ? lane : tid;
+    const int per = (a.B + counters - 1) / counters, b_lo = min(a.B, id * per), b_hi = min(a.B, b_lo + per);
+    int mine = 0;  // blocks of all samples are below 2^31
+#pragma unroll 4
     for (int i = b_lo; i < b_hi; ++i) mine += blocks_of(keys_of(a, i));
-    int64_t incl = mine;
+    int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(kFull, incl, o);
+      const int v = __shfl_up_sync(kFull, incl, o);
       if (lane >= o) incl += v;
     }
-    if (lane == 31) sm_scan[warp] = incl;
-    __syncthreads();
-    int64_t before = 0;
-    total = 0;
+    int before = 0, all = __shfl_sync(kFull, incl, 31);
+    if (!alone) {
+      if (lane == 31) sm_scan[warp] = incl;
+      __syncthreads();
+      all = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += sm_scan[w];
-      total += sm_scan[w];
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sm_scan[w];
+        all += sm_scan[w];
+      }
     }
-    total *= upb;
-    ctas = min((int64_t)gridDim.x, total);  // with at least a block each
-    c0 = min(total, blockIdx.x * total / ctas);
-    c1 = min(total, (blockIdx.x + 1) * total / ctas);
+    const int64_t total = (int64_t)all * upb, ctas = min((int64_t)gridDim.x, total);  // with at least a block each
+    share = quotient(total, ctas);
+    longer = total - share * ctas;
+    c0 = min(total, blockIdx.x * share + min((int64_t)blockIdx.x, longer));
+    c1 = min(total, c0 + share + (blockIdx.x < longer));
     if (!by_unit && tid == 0) splits[blockIdx.x].unit = -1;
-    int64_t off = (before + incl - mine) * upb;
-    if (c0 < c1 && c0 >= off && c0 < off + mine * upb) {
-      int i = b_lo;
-      for (;; ++i) {
-        const int64_t n = (int64_t)blocks_of(keys_of(a, i)) * upb;
+    if (c0 >= c1) return;
+    int64_t off = (int64_t)(before + incl - mine) * upb;
+    const bool here = c0 >= off && c0 < off + (int64_t)mine * upb;
+    b = b_lo;
+    if (here)
+      for (;; ++b) {
+        const int64_t n = (int64_t)blocks_of(keys_of(a, b)) * upb;
         if (c0 < off + n) break;
         off += n;
       }
-      sm_b = i;
-      sm_at = c0 - off;  // blocks into the sample's units
+    at = c0 - off;  // blocks into the sample's units
+    if (alone) {
+      const int who = __ffs(__ballot_sync(kFull, here)) - 1;
+      b = __shfl_sync(kFull, b, who);
+      at = __shfl_sync(kFull, at, who);
+    } else {
+      if (here) sm_b = b, sm_at = at;
+      __syncthreads();
+      b = sm_b;
+      at = sm_at;
     }
-    __syncthreads();
-    if (c0 >= c1) return;
-    b = sm_b;
-    at = sm_at;
   }
 
   // ---- one segment after another: the blocks of one unit that are this CTA's
@@ -280,7 +296,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
       look_end = a.mask ? min(a.mask_len, a.pt.max_pages * a.pt.page_size) : a.pt.max_pages * a.pt.page_size;
     } else {
       len = keys_of(a, b), nblk = blocks_of(len);
-      ub = (int)(at / nblk), blk0 = (int)(at - (int64_t)ub * nblk);
+      ub = (int)quotient(at, nblk), blk0 = (int)(at - (int64_t)ub * nblk);
       nseg = (int)min((int64_t)(nblk - blk0), c1 - c);
       key_0 = blk0 * S::kBlock + warp * S::kKeys;
       look_end = key_end = (int)min((int64_t)len, ((int64_t)blk0 + nseg) * S::kBlock);
@@ -584,6 +600,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
           make_uint2(CodeBf16::pack(x.x * inv, x.y * inv), CodeBf16::pack(x.z * inv, x.w * inv));
       if (d == 0 && a.lse) a.lse[at_out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     };
+#pragma unroll 2
     for (int i = tid; i < nh * (D / 4); i += kWarps * 32) {
       const int n = i / (D / 4), d = i % (D / 4) * 4;
       float mm = sm_m[0][n];
@@ -602,7 +619,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
         finish(n, d, x, mm, l);
       } else if constexpr (kCluster) {  // over warp 0's sum, which this thread alone has read
         *reinterpret_cast<float4 *>(sm_ring + (n * S::kHeadPitch + d) * 4) = x;
-        if (d == 0) sm_ml[0][n] = mm, sm_ml[1][n] = l;
+        if (d == 0) sm_ml[n] = make_float2(mm, l);
       } else {
         *reinterpret_cast<float4 *>(part + n * D + d) = x;
         if (d == 0) part[kHeadsPerUnit * D + 2 * n] = mm, part[kHeadsPerUnit * D + 2 * n + 1] = l;
@@ -610,26 +627,30 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
     }
     if constexpr (kCluster) {
       if (whole) return;
+      // Vectors of 4 dims in turn over the CTAs.  (Reading every warp's sums of the peers here,
+      // without the step above, measured slower: four times the remote bytes, 27 against 23 us
+      // for 128 robots.)
       cluster_sync();
       for (int i = rank * kWarps * 32 + tid; i < nh * (D / 4); i += cluster * kWarps * 32) {
         const int n = i / (D / 4), d = i % (D / 4) * 4;
-        float m[kMaxCluster], mm = -INFINITY, l = 0.0f;
-        float4 x = make_float4(0, 0, 0, 0), y[kMaxCluster];
-#pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) {
-          m[r] = -INFINITY;
-          if (r < cluster) {
-            m[r] = peer_load(at_peer(&sm_ml[0][n], r));
-            y[r] = peer_load4(at_peer(sm_ring + (n * S::kHeadPitch + d) * 4, r));
-          }
-          mm = fmaxf(mm, m[r]);
-        }
+        float2 ml[kMaxCluster];
+        float4 y[kMaxCluster], x = make_float4(0, 0, 0, 0);
+        float mm = -INFINITY, l = 0.0f;
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r)
           if (r < cluster) {
-            const float f = m[r] == -INFINITY ? 0.0f : ex2_approx(m[r] - mm);
+            ml[r] = peer_load2(at_peer(&sm_ml[n], r));
+            y[r] = peer_load4(at_peer(sm_ring + (n * S::kHeadPitch + d) * 4, r));
+          }
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < cluster) mm = fmaxf(mm, ml[r].x);
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < cluster) {
+            const float f = ml[r].x == -INFINITY ? 0.0f : ex2_approx(ml[r].x - mm);
             x.x += f * y[r].x, x.y += f * y[r].y, x.z += f * y[r].z, x.w += f * y[r].w;
-            l += f * peer_load(at_peer(&sm_ml[1][n], r));
+            l += f * ml[r].y;
           }
         finish(n, d, x, mm, l);
       }
@@ -638,11 +659,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
     }
     if (blk0 == 0 && tid == 0) {
       const int unit = b * upb + ub;
-      if (!whole)
-        splits[by_unit ? unit : blockIdx.x] =
-            Split{unit, (int)blockIdx.x, (int)(((c + nblk) * ctas - 1) / total), slot};
-      else if (by_unit && gridDim.x > 1)  // a lone CTA has no workspace and no second kernel
+      if (!whole) {
+        const int64_t end = c + nblk - 1, most = longer * (share + 1);  // its last block; those of the longer CTAs
+        const int64_t last = end < most ? quotient(end, share + 1) : longer + quotient(end - most, share);
+        splits[by_unit ? unit : blockIdx.x] = Split{unit, (int)blockIdx.x, (int)last, slot};
+      } else if (by_unit && gridDim.x > 1) {  // a lone CTA has no workspace and no second kernel
         splits[unit].unit = -1;
+      }
     }
     c += nseg;
     if (c >= c1) break;
@@ -654,94 +677,84 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
 
 // Adds up the parts of split unit blockIdx.x, in order of the keys.  A part is 8 heads x D/4
 // vectors; blockIdx.y takes an equal share of them, so that a few units with hundreds of
-// parts spread over many SMs.  Threads beyond a share's vectors take turns at the parts.
-// Bound by the L2's latency: the first parts are loaded while the weights are formed, the
-// others kAhead at a time.
+// parts spread over many SMs.  A share's vectors take `lanes` threads, and the block's groups
+// of so many threads take turns at the parts, each with a running maximum of its own, so that
+// one barrier is enough.  Bound by the L2's latency: kAhead parts are loaded at once.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_constant__ AttendArgs a, int grid) {
   pdl_wait();
   pdl_trigger();
-  constexpr int kAhead = 8, kStats = kHeadsPerUnit * D, kJoinWarps = kJoinThreads / 32;
-  constexpr int kAtOnce = kJoinThreads / kHeadsPerUnit;  // parts whose statistics are read at once
-  __shared__ float sm_w[kMaxGrid][kHeadsPerUnit], sm_l[kMaxGrid][kHeadsPerUnit];
-  __shared__ float sm_red[kJoinWarps][kHeadsPerUnit];
+  constexpr int kAhead = 8, kStats = kHeadsPerUnit * D;
   __shared__ float4 sm_x[kJoinThreads];
+  __shared__ float2 sm_ml[kJoinThreads];
   const Split sp = reinterpret_cast<const Split *>(a.part)[blockIdx.x];
   if (sp.unit < 0) return;
   const float *parts = a.part + grid * (sizeof(Split) / 4);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x;
   const int group = a.heads / a.kv, groups = head_groups(a.heads, a.kv), upb = a.kv * groups;
   const int b = sp.unit / upb, ub = sp.unit % upb, h0 = ub / groups * group + ub % groups * kHeadsPerUnit;
   const int nh = min(kHeadsPerUnit, group - ub % groups * kHeadsPerUnit);
   const int count = sp.last - sp.first + 1;
-  auto part_of = [&](int i) { return parts + (int64_t)(i == 0 ? sp.slot : 2 * (sp.first + i)) * kPartFloats<D>; };
-
-  const int lanes = 2 * D / gridDim.y, turns = kJoinThreads / lanes, turn = tid / lanes;  // lanes <= kJoinThreads
+  const int lanes = 2 * D / gridDim.y, turns = kJoinThreads / lanes, turn = tid / lanes;  // 4 <= lanes <= kJoinThreads
   const int v = blockIdx.y * lanes + tid % lanes, head = v / (D / 4);
   const bool mine = head < nh;
-  float4 ahead[kAhead];
-  auto load = [&](int j0) {
+
+  float m = -INFINITY, l = 0.0f;
+  float4 x = make_float4(0, 0, 0, 0);
+  auto add = [&](float m2, float l2, const float4 &y) {
+    const float mm = fmaxf(m, m2), f = m == -INFINITY ? 0.0f : ex2_approx(m - mm),
+                f2 = m2 == -INFINITY ? 0.0f : ex2_approx(m2 - mm);
+    x.x = f * x.x + f2 * y.x, x.y = f * x.y + f2 * y.y, x.z = f * x.z + f2 * y.z, x.w = f * x.w + f2 * y.w;
+    l = f * l + f2 * l2;
+    m = mm;
+  };
+  for (int j0 = turn; mine && j0 < count; j0 += kAhead * turns) {
+    float4 y[kAhead];
+    float2 ml[kAhead];
 #pragma unroll
     for (int q = 0; q < kAhead; ++q) {
       const int j = j0 + q * turns;
-      ahead[q] = make_float4(0, 0, 0, 0);
-      if (mine && j < count) ahead[q] = *reinterpret_cast<const float4 *>(part_of(j) + 4 * v);
+      if (j < count) {
+        const float *part = parts + (int64_t)(j == 0 ? sp.slot : 2 * (sp.first + j)) * kPartFloats<D>;
+        y[q] = *reinterpret_cast<const float4 *>(part + 4 * v);
+        ml[q] = *reinterpret_cast<const float2 *>(part + kStats + 2 * head);
+      }
     }
-  };
-  load(turn);
-
-  // weights of the parts, and the sum of their l
-  const int n = tid % kHeadsPerUnit;
-  float mm = -INFINITY;
-  if (n < nh)
-#pragma unroll 4
-    for (int i = tid / kHeadsPerUnit; i < count; i += kAtOnce) {
-      const float2 ml = *reinterpret_cast<const float2 *>(part_of(i) + kStats + 2 * n);
-      sm_w[i][n] = ml.x;
-      sm_l[i][n] = ml.y;
-      mm = fmaxf(mm, ml.x);
-    }
-  mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, 8));
-  mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, 16));
-  if (lane < 8) sm_red[warp][n] = mm;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) mm = fmaxf(mm, sm_red[w][n]);
-  __syncthreads();
-  float l = 0.0f;
-  if (n < nh)
-    for (int i = tid / kHeadsPerUnit; i < count; i += kAtOnce) {
-      const float m = sm_w[i][n], w = m == -INFINITY ? 0.0f : ex2_approx(m - mm);
-      sm_w[i][n] = w;
-      l += w * sm_l[i][n];
-    }
-  l += __shfl_xor_sync(kFull, l, 8);
-  l += __shfl_xor_sync(kFull, l, 16);
-  if (lane < 8) sm_red[warp][n] = l;
-  if (tid < kHeadsPerUnit) sm_l[0][n] = mm;  // only this thread read it
-  __syncthreads();
-
-  float4 x = make_float4(0, 0, 0, 0);
-  auto add = [&](float f, const float4 &y) { x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w; };
-  for (int j0 = turn; mine && j0 < count; j0 += kAhead * turns) {
-    if (j0 != turn) load(j0);
 #pragma unroll
     for (int q = 0; q < kAhead; ++q)
-      if (j0 + q * turns < count) add(sm_w[j0 + q * turns][head], ahead[q]);
+      if (j0 + q * turns < count) add(ml[q].x, ml[q].y, y[q]);
   }
+  // turns within a warp, then the rest through shared memory
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1)
+    if (o >= lanes) {
+      const float m2 = __shfl_xor_sync(kFull, m, o), l2 = __shfl_xor_sync(kFull, l, o);
+      const float4 y = make_float4(__shfl_xor_sync(kFull, x.x, o), __shfl_xor_sync(kFull, x.y, o),
+                                   __shfl_xor_sync(kFull, x.z, o), __shfl_xor_sync(kFull, x.w, o));
+      add(m2, l2, y);
+    }
   sm_x[tid] = x;
+  sm_ml[tid] = make_float2(m, l);
   __syncthreads();
   if (tid >= lanes || !mine) return;
+  const int step = max(lanes, 32);
+  for (int j = step; j < kJoinThreads; j += step) m = fmaxf(m, sm_ml[j + tid].x);
+  x = make_float4(0, 0, 0, 0);
   l = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) l += sm_red[w][head];
-  for (int j = 1; j < turns; ++j) add(1.0f, sm_x[j * lanes + tid]);
+#pragma unroll 8
+  for (int j = 0; j < kJoinThreads; j += step) {
+    const float2 ml = sm_ml[j + tid];
+    const float4 y = sm_x[j + tid];
+    const float f = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - m);
+    x.x += f * y.x, x.y += f * y.y, x.z += f * y.z, x.w += f * y.w;
+    l += f * ml.y;
+  }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   const int64_t at = (int64_t)b * a.heads + h0 + head;
   const int d = v % (D / 4) * 4;
   *reinterpret_cast<uint2 *>(a.out + at * D + d) =
       make_uint2(CodeBf16::pack(x.x * inv, x.y * inv), CodeBf16::pack(x.z * inv, x.w * inv));
-  if (d == 0 && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (sm_l[0][head] + log2f(l)) * 0.6931471805599453f;
+  if (d == 0 && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 namespace {
@@ -811,8 +824,12 @@ cudaError_t attend_go(const AttendArgs &a, cudaStream_t s) {
   if (e != cudaSuccess || p.grid == 1) return e;  // one CTA: nothing is split
   const int64_t units = (int64_t)a.B * a.kv * head_groups(a.heads, a.kv);
   const int lists = (int)(units < p.grid ? units : p.grid);
-  int shares = 1;  // about one CTA an SM in all, 16 vectors or more each
-  while (shares < D / 8 && lists * shares < 148) shares *= 2;
+  // Shares of a split unit: about one CTA an SM in all, of 16 vectors or more, of 4 where a unit
+  // has 128 parts or more (1 x 4096 keys in 64 parts: 8.8 us with 16 vectors, 10.0 with 4;
+  // 1 x 32768 in 256: 14.7 and 14.1).
+  const int finest = p.grid / lists >= 128 ? D / 2 : D / 8;
+  int shares = 1;
+  while (shares < finest && lists * shares * 2 <= 148) shares *= 2;
   return launch_pdl(k_attend_join<D>, dim3(lists, shares), kJoinThreads, 0, s, a, p.grid);
 }
 
