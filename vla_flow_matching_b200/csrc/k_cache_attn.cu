@@ -15,8 +15,9 @@
 // from there, so that two or three buffers of 8 KB are on their way at any time - 130 to 200
 // KB an SM, above what HBM's latency needs - and no barrier stands between warps until their
 // keys end.  (Loads straight into the products' registers, without shared memory, measured
-// slower: 54 against XXX us for 2 x 100k-131k bf16 keys.  A lane's share of V^T is 16 bytes of
-// four different rows, so a request of 8 lanes covers 32-byte pieces of 4 rows.)
+// the same for long bf16 keys and slower for 8-bit ones, 57 against 52 us for 24 samples of up to
+// 16k: a lane's share of V^T is 16 bytes of four different rows, so a request of 8 lanes covers
+// 32-byte pieces of 4 rows.)
 #include "cache.cuh"
 #include "common.cuh"
 #include "kernels.cuh"
@@ -32,7 +33,7 @@ constexpr int kWarps = 4;
 constexpr int kHeadsPerUnit = 8;  // query heads of one kv head that share a pass: the product's columns
 constexpr int kJoinThreads = 512;
 constexpr float kWeightBits = 15.0f;
-constexpr int kMaxCluster = 8, kClusterBlocks = 8;
+constexpr int kMaxCluster = 8, kClusterBlocks = 16;
 constexpr unsigned kFull = 0xffffffffu;
 
 // Four 8x8 matrices of 16-bit elements, lane i's address the row i % 8 of matrix i / 8.
@@ -760,12 +761,14 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
 namespace {
 
 // How a call is shared out (see above).  A cluster's CTAs may get more blocks than an even
-// share, if its unit is long for 8 of them; the even way pays for its scan, its parts and the
-// second kernel, about as much as three blocks of a CTA.  Clusters where that is the larger
-// cost, and only while the even share is small: with more work the second kernel is hidden
-// and ragged samples keep the CTAs of a cluster waiting (lengths are not known here: the
-// page tables' are taken).  GPU time of a call, clusters against even shares: 1 x 816 bf16
-// keys XXX, 128 x 600-816 YYY, 1 x 4096 ZZZ us.
+// share, if its unit is long for 8 of them or the clusters do not fill whole waves of CTAs; the
+// even way pays for its scan, its parts and the second kernel, about as much as 192 KB of keys
+// and values in every CTA.  Clusters where that is the larger cost, and only while the even
+// share is small: with more work the second kernel hardly shows, and ragged samples keep the CTAs
+// of a cluster waiting (lengths are not known here: the page tables' are taken).  GPU time of a
+// call in us, clusters / even shares: 1 x 816 bf16 keys of 256 dims 7.2 / 8.7, 1 x 4096
+// 13.7 / 8.9, 40 x 1000-2000 18.4 / 21.3, 128 x 600-816 22.5 / 26.1, 256 x 600-816 36.7 /
+// 44.5; 512 x 300-700 int8 keys of 64 dims 14.3 / 24.3.
 struct Plan {
   int cluster;  // CTAs of a cluster, 0: even shares and a join
   int grid;
@@ -777,8 +780,10 @@ Plan attend_plan(int B, int heads, int kv, int page_size, int max_pages) {
   const int64_t units = (int64_t)B * kv * head_groups(heads, kv);
   int cluster = 1;
   while (cluster < kMaxCluster && cluster < blocks && units * cluster * 2 <= S::kGrid) cluster *= 2;
-  const int64_t even = (units * blocks + S::kGrid - 1) / S::kGrid, mine = (blocks + cluster - 1) / cluster;
-  if (even <= kClusterBlocks && mine <= even + 3) return Plan{cluster, (int)(units * cluster)};
+  const int64_t even = (units * blocks + S::kGrid - 1) / S::kGrid;
+  const int64_t waves = (units * cluster + S::kGrid - 1) / S::kGrid, mine = waves * ((blocks + cluster - 1) / cluster);
+  const int slack = (192 << 10) / (2 * S::kBlock * S::kRowBytes);
+  if (even <= kClusterBlocks && mine <= even + slack) return Plan{cluster, (int)(units * cluster)};
   return Plan{0, (int)(units * blocks < S::kGrid ? units * blocks : S::kGrid)};
 }
 template <typename C, int D>
