@@ -164,7 +164,8 @@ __device__ __forceinline__ void turn_cos_sin_approx(uint32_t turn, float &c, flo
 template <typename T, int D, bool kExact>
 struct RowMath {
   static constexpr int kN = Vec<T>::kN, kP = kN / 2, kLanes = D / 2 / kN;
-  f32x2 c[kP], s[kP], ns[kP];  // cosines, sines and their negatives of the lane's pairs
+  f32x2 c[kP], s[kP];           // cosines and sines of the lane's pairs
+  f32x2 ns[kExact ? kP : 1];    // kExact: negative sines, which save a rounding
 
   // The tables in shared memory are laid out so that the lanes of a group read consecutive
   // words: entry i of lane l is turn i * kLanes + l; gains go four at a time.
@@ -189,13 +190,17 @@ struct RowMath {
       }
       c[i] = pair(cs[0], cs[1]);
       s[i] = pair(sn[0], sn[1]);
-      ns[i] = pair(-sn[0], -sn[1]);
+      if constexpr (kExact) ns[i] = pair(-sn[0], -sn[1]);
     }
   }
   __device__ __forceinline__ void rotate(f32x2 (&x)[kP], f32x2 (&y)[kP]) const {
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
-      const f32x2 v = fma2(y[i], ns[i], mul2(x[i], c[i]));
+      f32x2 v;
+      if constexpr (kExact)
+        v = fma2(y[i], ns[i], mul2(x[i], c[i]));
+      else
+        v = fma2(mul2(y[i], s[i]), pair(-1.0f, -1.0f), mul2(x[i], c[i]));
       y[i] = fma2(y[i], c[i], mul2(x[i], s[i]));
       x[i] = v;
     }
@@ -230,24 +235,25 @@ struct RowMath {
   }
 };
 
-// Three kinds of blocks, in this order: blocks of q rows, of k rows (rotated into k_out), or,
-// with a cache, of k and v rows on their way into pages.  An item of the first two is `per`
-// heads of one token: a group of lanes forms the token's cosines and sines once for them and
-// keeps the next kAhead rows on their way; an item of the third is one head's key and value.
-// One item a group, so that the rows are on their way before anything else is read, and
-// blocks of padding (tokens beyond a sample's count) end at once.  Bound by HBM at size and
-// not far from it by instructions (packed fp32 where it can be): 32 prefixes of 816 tokens,
-// 9 rows of 512 bytes each, move 241 MB.
-template <typename T, typename Pool, int D>
-__global__ void __launch_bounds__(256, 3) k_rows(const __grid_constant__ RowArgs a) {
+// Kinds of blocks, in this order: of q rows, of k rows (rotated into k_out), or, with kPages,
+// of k and v rows on their way into pages (kTurned: there are blocks of the first two kinds).
+// An item of the first two is `per` heads of one token: a group of lanes forms the token's
+// cosines and sines once for them and keeps the next kAhead rows on their way; an item of the
+// third is one head's key and value.  One item a group, so that the rows are on their way
+// before anything else is read, and blocks of padding (tokens beyond a sample's count) end at
+// once.  Bound by HBM at size and not far from it by instructions (packed fp32 where it can
+// be): 32 prefixes of 816 tokens, 9 rows of 512 bytes each, move 241 MB in 42 us; 64 padded ones
+// of 2 rows go into e4m3 pages in 17 us.
+template <typename T, typename Pool, int D, bool kTurned, bool kPages>
+__global__ void __launch_bounds__(256, kTurned ? 3 : 4) k_rows(const __grid_constant__ RowArgs a) {
   using M = RowMath<T, D, sizeof(T) == 4 || Pool::kScaled>;
-  constexpr int kN = M::kN, kP = M::kP, kLanes = M::kLanes, kGroups = 256 / kLanes, kAhead = 3;
+  constexpr int kN = M::kN, kP = M::kP, kLanes = M::kLanes, kGroups = 256 / kLanes, kAhead = kTurned ? 3 : 2;
   __shared__ uint64_t sm_turn[D / 2];  // lanes index it apart: from the parameters that would be one after another
   __shared__ __align__(16) float sm_gain[D];  // 1 + gain
   pdl_wait();
   pdl_trigger();
-  const bool is_q = blockIdx.x < a.q_blocks;
-  const bool to_pages = !is_q && a.to_cache;
+  const bool is_q = kTurned && blockIdx.x < a.q_blocks;
+  const bool to_pages = kPages && !is_q;
   const uint32_t block = is_q ? blockIdx.x : blockIdx.x - a.q_blocks;
   const uint32_t item = block * kGroups + threadIdx.x / kLanes;
   const int l0 = threadIdx.x % kLanes * kN;
@@ -273,6 +279,7 @@ __global__ void __launch_bounds__(256, 3) k_rows(const __grid_constant__ RowArgs
   if (to_pages) {
     load(0, src, kept);
     load(1, (const T *)a.v.data + (kept ? b * a.v.sb + t * a.v.st + h0 * a.v.sh + l0 : 0), kept);
+    if (a.count && !__syncthreads_or(kept)) return;
   } else {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
@@ -287,79 +294,83 @@ __global__ void __launch_bounds__(256, 3) k_rows(const __grid_constant__ RowArgs
     for (int i = threadIdx.x; i < D / 2; i += 256) sm_turn[M::turn_at(i)] = a.turn[i];
   if (gain)
     for (int i = threadIdx.x; i < D; i += 256) sm_gain[M::gain_at(i)] = 1.0f + gain[i];
-  if (!__syncthreads_or(kept)) return;
+  __syncthreads();
   M math;
   if (a.rotate) math.turn(pos, sm_turn + l0 / kN);
 
-  if (!to_pages) {
-    const RowsPtr &to = is_q ? a.q_out : a.k_out;
-    T *dst = (T *)to.data + (kept ? b * to.sb + t * to.st + h0 * to.sh + l0 : 0);
-    for (int r0 = 0; r0 < per; r0 += kAhead) {
+  if constexpr (kTurned) {
+    if (!to_pages) {
+      const RowsPtr &to = is_q ? a.q_out : a.k_out;
+      T *dst = (T *)to.data + (kept ? b * to.sb + t * to.st + h0 * to.sh + l0 : 0);
+      for (int r0 = 0; r0 < per; r0 += kAhead) {
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        if (r0 + j >= per) break;  // the same for all: the exchanges below are warp-wide
-        f32x2 x[kP], y[kP];
-        Vec<T>::get(lo[j], x);
-        Vec<T>::get(hi[j], y);
-        load(j, src, r0 + j + kAhead < n);
-        src += in.sh;
-        if (gain) M::norm(x, y, sm_gain + l0 / kN * 4, a.eps);
-        if (a.rotate) math.rotate(x, y);
-        float u[kN], v[kN];
-        M::floats(x, u);
-        M::floats(y, v);
-        if (r0 + j < n) {
-          *reinterpret_cast<uint4 *>(dst) = Vec<T>::put(u);
-          *reinterpret_cast<uint4 *>(dst + D / 2) = Vec<T>::put(v);
-        }
-        dst += to.sh;
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {  // the key, the value
-    f32x2 x[kP], y[kP];
-    Vec<T>::get(lo[j], x);
-    Vec<T>::get(hi[j], y);
-    if (j == 0 && gain) M::norm(x, y, sm_gain + l0 / kN * 4, a.eps);
-    if (j == 0 && a.rotate) math.rotate(x, y);
-    float u[kN], v[kN];
-    M::floats(x, u);
-    M::floats(y, v);
-    const PoolPtr &pool = j ? a.vp : a.kp;
-    const int64_t at = (int64_t)cell * a.hk + h0;
-    if constexpr (Pool::kScaled) {
-      float most = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kN; ++i) most = max_nan(max_nan(most, fabsf(u[i])), fabsf(v[i]));
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(kFull, most, o));
-      if (cell >= 0) {
-        const uint32_t top = __float_as_uint(most);
-        const bool finite = top < 0x7f800000u;
-        const float scale = finite ? Pool::scale(top) : __uint_as_float(0x7fc00000u);
-        uint32_t w[kN / 4] = {}, w2[kN / 4] = {};
-        if (finite)
-#pragma unroll
-          for (int i = 0; i < kN / 4; ++i) {
-            w[i] = Pool::codes(u + 4 * i, scale);
-            w2[i] = Pool::codes(v + 4 * i, scale);
+        for (int j = 0; j < kAhead; ++j) {
+          if (r0 + j >= per) break;  // the same for all: the exchanges below are warp-wide
+          f32x2 x[kP], y[kP];
+          Vec<T>::get(lo[j], x);
+          Vec<T>::get(hi[j], y);
+          load(j, src, r0 + j + kAhead < n);
+          src += in.sh;
+          if (gain) M::norm(x, y, sm_gain + l0 / kN * 4, a.eps);
+          if (a.rotate) math.rotate(x, y);
+          float u[kN], v[kN];
+          M::floats(x, u);
+          M::floats(y, v);
+          if (r0 + j < n) {
+            *reinterpret_cast<uint4 *>(dst) = Vec<T>::put(u);
+            *reinterpret_cast<uint4 *>(dst + D / 2) = Vec<T>::put(v);
           }
-        uint8_t *dst = (uint8_t *)pool.codes + at * D + l0;
-        if constexpr (kN == 8) {
-          *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
-          *reinterpret_cast<uint2 *>(dst + D / 2) = make_uint2(w2[0], w2[1]);
-        } else {
-          *reinterpret_cast<uint32_t *>(dst) = w[0];
-          *reinterpret_cast<uint32_t *>(dst + D / 2) = w2[0];
+          dst += to.sh;
         }
-        if (l0 == 0) pool.scale[at] = scale;
       }
-    } else if (cell >= 0) {
-      bf16 *dst = (bf16 *)pool.codes + at * D + l0;
-      store_bf16(dst, u);
-      store_bf16(dst + D / 2, v);
+      return;
+    }
+  }
+  if constexpr (kPages) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {  // the key, the value
+      f32x2 x[kP], y[kP];
+      Vec<T>::get(lo[j], x);
+      Vec<T>::get(hi[j], y);
+      if (j == 0 && gain) M::norm(x, y, sm_gain + l0 / kN * 4, a.eps);
+      if (j == 0 && a.rotate) math.rotate(x, y);
+      float u[kN], v[kN];
+      M::floats(x, u);
+      M::floats(y, v);
+      const PoolPtr &pool = j ? a.vp : a.kp;
+      const int64_t at = (int64_t)cell * a.hk + h0;
+      if constexpr (Pool::kScaled) {
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) most = max_nan(max_nan(most, fabsf(u[i])), fabsf(v[i]));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(kFull, most, o));
+        if (cell >= 0) {
+          const uint32_t top = __float_as_uint(most);
+          const bool finite = top < 0x7f800000u;
+          const float scale = finite ? Pool::scale(top) : __uint_as_float(0x7fc00000u);
+          uint32_t w[kN / 4] = {}, w2[kN / 4] = {};
+          if (finite)
+#pragma unroll
+            for (int i = 0; i < kN / 4; ++i) {
+              w[i] = Pool::codes(u + 4 * i, scale);
+              w2[i] = Pool::codes(v + 4 * i, scale);
+            }
+          uint8_t *dst = (uint8_t *)pool.codes + at * D + l0;
+          if constexpr (kN == 8) {
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+            *reinterpret_cast<uint2 *>(dst + D / 2) = make_uint2(w2[0], w2[1]);
+          } else {
+            *reinterpret_cast<uint32_t *>(dst) = w[0];
+            *reinterpret_cast<uint32_t *>(dst + D / 2) = w2[0];
+          }
+          if (l0 == 0) pool.scale[at] = scale;
+        }
+      } else if (cell >= 0) {
+        bf16 *dst = (bf16 *)pool.codes + at * D + l0;
+        store_bf16(dst, u);
+        store_bf16(dst + D / 2, v);
+      }
     }
   }
 }
@@ -452,7 +463,10 @@ cudaError_t rows_go(RowArgs a, cudaStream_t s) {
   a.by_k = FastDiv(nk ? nk : 1);
   a.by_t = FastDiv(a.T);
   a.q_blocks = blocks(nq);
-  return launch_pdl(k_rows<T, Pool, D>, dim3(a.q_blocks + blocks(nk)), 256, 0, s, a);
+  const dim3 grid(a.q_blocks + blocks(nk));
+  if (!a.to_cache) return launch_pdl(k_rows<T, PoolBf16, D, true, false>, grid, 256, 0, s, a);
+  if (a.hq) return launch_pdl(k_rows<T, Pool, D, true, true>, grid, 256, 0, s, a);
+  return launch_pdl(k_rows<T, Pool, D, false, true>, grid, 256, 0, s, a);
 }
 template <typename T, typename Pool, int D>
 cudaError_t read_go(ReadArgs a, cudaStream_t s) {
