@@ -174,7 +174,8 @@ typedef struct {
  * each head's row where a gain is given, then the rotate-half rotation of the pairs
  * (i, i + head_dim/2) by pos * rope_base^(-2i/head_dim) where rope_base > 0 (1 or
  * more).  The angle is exact to 2^-32 of a turn at every 32-bit position; all of it
- * is fp32, rounded once to the output's type. */
+ * is fp32 (sines and cosines of bf16 rows that stay bf16 to 2^-20), rounded once to
+ * the output's type. */
 typedef struct {
   const float *q_gain, *k_gain;  /* (head_dim) fp32; NULL: no norm */
   const int32_t *positions;      /* (B, T); NULL: start[b] + t */
