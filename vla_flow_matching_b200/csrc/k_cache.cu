@@ -80,12 +80,15 @@ __device__ __forceinline__ void store_bf16(bf16 *p, const float (&v)[N]) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 
-// Pool element types: bf16 rows as they are, or codes of a scaled row.
+// Pool element types: bf16 rows as they are, or codes of a scaled row.  kDouble: keys are normed
+// and rotated in 64 bits on their way in.  What e4m3 codes stand for is exact, so all the error
+// of a page is in codes next to the border of two, a whole step each; in fp32 one value in 2.5
+// million falls on the wrong side, in 64 bits next to none.
 struct PoolBf16 {
-  static constexpr bool kScaled = false;
+  static constexpr bool kScaled = false, kDouble = false;
 };
 struct PoolE4m3 {
-  static constexpr bool kScaled = true;
+  static constexpr bool kScaled = true, kDouble = true;
   // Least power of two that brings `top` within 448 = 1.75 * 2^8: a power of two makes
   // the division exact, so a code depends on its value alone, and what a code stands
   // for is exact in bf16.  top = f * 2^e, 1 <= f < 2: 2^(e-8), or 2^(e-7) above 1.75.
@@ -107,7 +110,7 @@ struct PoolE4m3 {
   }
 };
 struct PoolInt8 {
-  static constexpr bool kScaled = true;
+  static constexpr bool kScaled = true, kDouble = false;
   static __device__ __forceinline__ float scale(uint32_t top) {
     return fmaxf(__fdiv_rn(__uint_as_float(top), 127.0f), kMinScale);
   }
@@ -159,8 +162,7 @@ __device__ __forceinline__ void turn_cos_sin_approx(uint32_t turn, float &c, flo
 
 // A lane holds 16 bytes of each half of a row, the pairs (i, i + D/2), so the rotation needs
 // no exchange; D/16 (bf16) or D/8 (fp32) lanes hold a row.  RowMath has what is done to a row.
-// kExact: sines and cosines to fp32 (fp32 rows, and 8-bit codes, where an error next to the
-// border of two codes becomes a step between them).
+// kExact: sines and cosines to fp32 (fp32 rows, and those on their way into 8-bit codes).
 template <typename T, int D, bool kExact>
 struct RowMath {
   static constexpr int kN = Vec<T>::kN, kP = kN / 2, kLanes = D / 2 / kN;
@@ -235,6 +237,63 @@ struct RowMath {
   }
 };
 
+// cos and sin of 2 pi t 2^-64 as turn_cos_sin, to 2^-32: the Taylor terms from y^5 and y^6 on are
+// small enough for fp32 (below 2^-8, so their roundings below 2^-32), the others are in 64 bits.
+__device__ __forceinline__ void turn_cos_sin(uint64_t t, double &c, double &s) {
+  const uint64_t quarter = (t + (1ull << 61)) >> 62;
+  const double y = (double)(int64_t)(t - (quarter << 62)) * 3.4061215800304616e-19;  // 2 pi 2^-64
+  const double z = y * y;
+  const float w = (float)z;
+  const float st = 1.0f / 120 + w * (-1.0f / 5040 + w * (1.0f / 362880 + w * (-1.0f / 39916800)));
+  const float ct = -1.0f / 720 + w * (1.0f / 40320 + w * (-1.0f / 3628800 + w * (1.0f / 479001600)));
+  const double sp = fma(y * z, fma((double)st, z, -1.0 / 6), y);
+  const double cp = fma(fma(fma((double)ct, z, 1.0 / 24), z, -0.5), z, 1.0);
+  const double a = (quarter & 1) ? sp : cp, b = (quarter & 1) ? cp : sp;
+  c = ((quarter + 1) & 2) ? -a : a;
+  s = (quarter & 2) ? -b : b;
+}
+// x to fp32, rounded to odd: towards zero, with the last bit set where that lost something, so that
+// a later rounding to fewer bits (twice as few or more) is that of x itself.  (Below 2^-126, where
+// a code is zero whatever the last bits are, the lost bits are not all looked at.)
+__device__ __forceinline__ float to_odd(double x) {
+  const uint32_t lost = __double2loint(x) & 0x1fffffffu;
+  return __uint_as_float(__float_as_uint(__double2float_rz(x)) | (lost != 0));
+}
+// A lane's share of a row normed (gain, or nullptr) and rotated (table, or nullptr) in 64 bits.
+template <typename M, int D, int kN>
+__device__ __forceinline__ void turn_double(float (&u)[kN], float (&v)[kN], const float *gain, float eps, int64_t pos,
+                                            const uint64_t *table) {
+  double x[kN], y[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) x[i] = u[i], y[i] = v[i];
+  if (gain) {
+    double ss = 0.0;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) ss = fma(x[i], x[i], fma(y[i], y[i], ss));
+#pragma unroll
+    for (int o = M::kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+    const double inv = rsqrt(ss * (1.0 / D) + (double)eps);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int at = i / 4 * 4 * M::kLanes + i % 4;
+      x[i] *= inv * (1.0 + (double)gain[at]);
+      y[i] *= inv * (1.0 + (double)gain[D / 2 + at]);
+    }
+  }
+  if (table) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      double c, s;
+      turn_cos_sin((uint64_t)pos * table[i * M::kLanes], c, s);
+      const double w = x[i] * c - y[i] * s;
+      y[i] = y[i] * c + x[i] * s;
+      x[i] = w;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kN; ++i) u[i] = to_odd(x[i]), v[i] = to_odd(y[i]);
+}
+
 // Kinds of blocks, in this order: of q rows, of k rows (rotated into k_out), or, with kPages,
 // of k and v rows on their way into pages (kTurned: there are blocks of the first two kinds).
 // An item of the first two is `per` heads of one token: a group of lanes forms the token's
@@ -243,13 +302,13 @@ struct RowMath {
 // before anything else is read, and blocks of padding (tokens beyond a sample's count) end at
 // once.  Bound by HBM at size and not far from it by instructions (packed fp32 where it can
 // be): 32 prefixes of 816 tokens, 9 rows of 512 bytes each, move 241 MB in 42 us; 64 padded ones
-// of 2 rows go into e4m3 pages in 17 us.
+// of 2 rows go into e4m3 pages in 21 us (17 with the keys turned in fp32).
 template <typename T, typename Pool, int D, bool kTurned, bool kPages>
 __global__ void __launch_bounds__(256, kTurned ? 3 : 4) k_rows(const __grid_constant__ RowArgs a) {
   using M = RowMath<T, D, sizeof(T) == 4 || Pool::kScaled>;
   constexpr int kN = M::kN, kP = M::kP, kLanes = M::kLanes, kGroups = 256 / kLanes, kAhead = kTurned ? 3 : 2;
   __shared__ uint64_t sm_turn[D / 2];  // lanes index it apart: from the parameters that would be one after another
-  __shared__ __align__(16) float sm_gain[D];  // 1 + gain
+  __shared__ __align__(16) float sm_gain[D];  // 1 + gain (in 64 bits: the gain)
   pdl_wait();
   pdl_trigger();
   const bool is_q = kTurned && blockIdx.x < a.q_blocks;
@@ -293,10 +352,11 @@ __global__ void __launch_bounds__(256, kTurned ? 3 : 4) k_rows(const __grid_cons
   if (a.rotate)
     for (int i = threadIdx.x; i < D / 2; i += 256) sm_turn[M::turn_at(i)] = a.turn[i];
   if (gain)
-    for (int i = threadIdx.x; i < D; i += 256) sm_gain[M::gain_at(i)] = 1.0f + gain[i];
+    for (int i = threadIdx.x; i < D; i += 256)
+      sm_gain[M::gain_at(i)] = Pool::kDouble && to_pages ? gain[i] : 1.0f + gain[i];
   __syncthreads();
   M math;
-  if (a.rotate) math.turn(pos, sm_turn + l0 / kN);
+  if (a.rotate && !(Pool::kDouble && to_pages)) math.turn(pos, sm_turn + l0 / kN);
 
   if constexpr (kTurned) {
     if (!to_pages) {
@@ -332,11 +392,17 @@ __global__ void __launch_bounds__(256, kTurned ? 3 : 4) k_rows(const __grid_cons
       f32x2 x[kP], y[kP];
       Vec<T>::get(lo[j], x);
       Vec<T>::get(hi[j], y);
-      if (j == 0 && gain) M::norm(x, y, sm_gain + l0 / kN * 4, a.eps);
-      if (j == 0 && a.rotate) math.rotate(x, y);
+      if constexpr (!Pool::kDouble) {
+        if (j == 0 && gain) M::norm(x, y, sm_gain + l0 / kN * 4, a.eps);
+        if (j == 0 && a.rotate) math.rotate(x, y);
+      }
       float u[kN], v[kN];
       M::floats(x, u);
       M::floats(y, v);
+      if constexpr (Pool::kDouble)
+        if (j == 0 && (gain || a.rotate))
+          turn_double<M, D>(u, v, gain ? sm_gain + l0 / kN * 4 : nullptr, a.eps, pos,
+                            a.rotate ? sm_turn + l0 / kN : nullptr);
       const PoolPtr &pool = j ? a.vp : a.kp;
       const int64_t at = (int64_t)cell * a.hk + h0;
       if constexpr (Pool::kScaled) {
