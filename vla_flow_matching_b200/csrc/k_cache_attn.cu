@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
   auto blocks_of = [](int len) { return max(1, (int)(((uint32_t)len + S::kBlock - 1) / S::kBlock)); };
 
   // ---- this CTA's blocks [c0, c1), its first sample, and where in the sample's units it starts
-  int b;
+  int b, held = 0;  // up to 32 samples: lane i holds the keys of sample i
   int64_t c0, c1, at, share = 1, longer = 0;  // a CTA's blocks; the first `longer` CTAs have one more
   Split *splits = reinterpret_cast<Split *>(a.part);
   float *parts = a.part + gridDim.x * (sizeof(Split) / 4);
@@ -238,8 +238,13 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
     const int counters = alone ? 32 : kWarps * 32, id = alone ? lane : tid;
     const int per = (a.B + counters - 1) / counters, b_lo = min(a.B, id * per), b_hi = min(a.B, b_lo + per);
     int mine = 0;  // blocks of all samples are below 2^31
+    if (a.B <= 32) {
+      held = lane < a.B ? keys_of(a, lane) : 0;
+      mine = lane < a.B ? blocks_of(held) : 0;
+    } else {
 #pragma unroll 4
-    for (int i = b_lo; i < b_hi; ++i) mine += blocks_of(keys_of(a, i));
+      for (int i = b_lo; i < b_hi; ++i) mine += blocks_of(keys_of(a, i));
+    }
     int incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
     int64_t off = (int64_t)(before + incl - mine) * upb;
     const bool here = c0 >= off && c0 < off + (int64_t)mine * upb;
     b = b_lo;
-    if (here)
+    if (here && a.B > 32)
       for (;; ++b) {
         const int64_t n = (int64_t)blocks_of(keys_of(a, b)) * upb;
         if (c0 < off + n) break;
@@ -296,7 +301,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
       key_0 = rank * S::kBlock + warp * S::kKeys;
       look_end = a.mask ? min(a.mask_len, a.pt.max_pages * a.pt.page_size) : a.pt.max_pages * a.pt.page_size;
     } else {
-      len = keys_of(a, b), nblk = blocks_of(len);
+      len = a.B <= 32 ? __shfl_sync(kFull, held, b) : keys_of(a, b), nblk = blocks_of(len);
       ub = (int)quotient(at, nblk), blk0 = (int)(at - (int64_t)ub * nblk);
       nseg = (int)min((int64_t)(nblk - blk0), c1 - c);
       key_0 = blk0 * S::kBlock + warp * S::kKeys;
