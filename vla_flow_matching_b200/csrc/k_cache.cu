@@ -441,52 +441,58 @@ __global__ void __launch_bounds__(256, kTurned ? 3 : 4) k_rows(const __grid_cons
   }
 }
 
-// A group of lanes moves a row of keys and the row of values beside it, 16 bytes of
-// output a lane (8 bf16 or 4 fp32 values), and kAtOnce such pairs at once, whose loads are on
-// their way together.  Bound by HBM: 18 layers of 16 prefixes of 560 tokens move 321 MB.
+// A group of lanes moves a row of keys and the row of values beside it: a lane has kChunks pieces
+// of each, 16 bytes of output (8 bf16 or 4 fp32 values) and kLanes pieces apart, so that loads
+// and stores are consecutive over the lanes, and kAtOnce such pairs of rows on their way
+// together.  Bound by HBM: 18 layers of 16 prefixes of 560 tokens move 321 MB.
 template <typename T, typename Pool, int D>
 __global__ void __launch_bounds__(256) k_cache_read(const __grid_constant__ ReadArgs a) {
   pdl_wait();
   pdl_trigger();
-  constexpr int kN = Vec<T>::kN, kLanes = D / kN, kAtOnce = 2, kWords = kN * (Pool::kScaled ? 1 : 2) / 4;
+  constexpr int kN = Vec<T>::kN, kChunks = 2, kLanes = D / kN / kChunks, kAtOnce = 2;
+  constexpr int kWords = kN * (Pool::kScaled ? 1 : 2) / 4, kBytes = Pool::kScaled ? 1 : 2;
   const uint32_t items = (uint32_t)a.layers * a.B * a.kv * a.P;  // below 2^31
   const uint32_t step = gridDim.x * (256 / kLanes);
   const int l0 = threadIdx.x % kLanes * kN;
   for (uint32_t first = blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes; first < items; first += kAtOnce * step) {
-    int cell[kAtOnce], h[kAtOnce], layer[kAtOnce];
+    int64_t at[kAtOnce];  // row of the pools, -1: zeros
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       const uint32_t item = first + u * step;
-      cell[u] = -1;
+      at[u] = -1;
       if (item < items) {
-        const uint32_t rest = a.by_p.div(item), up = a.by_kv.div(rest);
-        layer[u] = (int)a.by_b.div(up);
-        h[u] = (int)(rest - up * a.kv);
-        const int p = (int)(item - rest * a.P), b = (int)(up - layer[u] * a.B);
-        if (p < a.lens[b] && (!a.mask || a.mask[(int64_t)b * a.P + p])) cell[u] = cache_row(a.pt, b, p);
-        if (a.mask_out && layer[u] == 0 && h[u] == 0 && l0 == 0) a.mask_out[(int64_t)b * a.P + p] = cell[u] >= 0;
+        const uint32_t rest = a.by_p.div(item), up = a.by_kv.div(rest), layer = a.by_b.div(up);
+        const int h = (int)(rest - up * a.kv), p = (int)(item - rest * a.P), b = (int)(up - layer * a.B);
+        int cell = -1;
+        if (p < a.lens[b] && (!a.mask || a.mask[(int64_t)b * a.P + p])) cell = cache_row(a.pt, b, p);
+        if (a.mask_out && layer == 0 && h == 0 && l0 == 0) a.mask_out[(int64_t)b * a.P + p] = cell >= 0;
+        if (cell >= 0) at[u] = (layer * a.layer_rows + cell) * a.kv + h;
       }
     }
-    uint32_t w[kAtOnce][2][kWords];  // codes of the lane's values
+    uint32_t w[kAtOnce][2][kChunks][kWords];  // codes of the lane's values
     float scale[kAtOnce][2];
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int j = 0; j < kWords; ++j) w[u][i][j] = 0;
+        const PoolPtr &pool = i ? a.vp : a.kp;
+        const uint8_t *p = (const uint8_t *)pool.codes + (at[u] * D + l0) * kBytes;
         scale[u][i] = 0.0f;
-        if (cell[u] >= 0) {
-          const PoolPtr &pool = i ? a.vp : a.kp;
-          const int64_t at = (layer[u] * a.layer_rows + cell[u]) * a.kv + h[u];
-          const uint8_t *p = (const uint8_t *)pool.codes + (at * D + l0) * (Pool::kScaled ? 1 : 2);
-          if constexpr (kWords == 4)
-            *reinterpret_cast<uint4 *>(w[u][i]) = *reinterpret_cast<const uint4 *>(p);
-          else if constexpr (kWords == 2)
-            *reinterpret_cast<uint2 *>(w[u][i]) = *reinterpret_cast<const uint2 *>(p);
-          else
-            w[u][i][0] = *reinterpret_cast<const uint32_t *>(p);
-          if constexpr (Pool::kScaled) scale[u][i] = pool.scale[at];
+        if constexpr (Pool::kScaled)
+          if (at[u] >= 0) scale[u][i] = pool.scale[at[u]];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) w[u][i][c][j] = 0;
+          if (at[u] >= 0) {
+            const uint8_t *q = p + c * kLanes * kN * kBytes;
+            if constexpr (kWords == 4)
+              *reinterpret_cast<uint4 *>(w[u][i][c]) = *reinterpret_cast<const uint4 *>(q);
+            else if constexpr (kWords == 2)
+              *reinterpret_cast<uint2 *>(w[u][i][c]) = *reinterpret_cast<const uint2 *>(q);
+            else
+              w[u][i][c][0] = *reinterpret_cast<const uint32_t *>(q);
+          }
         }
       }
 #pragma unroll
@@ -495,18 +501,30 @@ __global__ void __launch_bounds__(256) k_cache_read(const __grid_constant__ Read
       if (item >= items) break;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float x[kN];
-        if constexpr (Pool::kScaled) {
+        T *dst = (T *)(i ? a.v_out : a.k_out) + (int64_t)item * D + l0;
 #pragma unroll
-          for (int j = 0; j < kWords; ++j) Pool::values(w[u][i][j], x + 4 * j);
+        for (int c = 0; c < kChunks; ++c) {
+          uint4 out;
+          if constexpr (!Pool::kScaled && sizeof(T) == 2) {
+            out = *reinterpret_cast<const uint4 *>(w[u][i][c]);  // bits as they are
+          } else {
+            float x[kN];
+            if constexpr (Pool::kScaled) {
 #pragma unroll
-          for (int j = 0; j < kN; ++j) x[j] *= scale[u][i];
-        } else {
+              for (int j = 0; j < kWords; ++j) Pool::values(w[u][i][c][j], x + 4 * j);
 #pragma unroll
-          for (int j = 0; j < kWords; ++j)
-            x[2 * j] = __uint_as_float(w[u][i][j] << 16), x[2 * j + 1] = __uint_as_float(w[u][i][j] & 0xffff0000u);
+              for (int j = 0; j < kN; ++j) x[j] *= scale[u][i];
+            } else {
+#pragma unroll
+              for (int j = 0; j < kWords; ++j) {
+                x[2 * j] = __uint_as_float(w[u][i][c][j] << 16);
+                x[2 * j + 1] = __uint_as_float(w[u][i][c][j] & 0xffff0000u);
+              }
+            }
+            out = Vec<T>::put(x);
+          }
+          *reinterpret_cast<uint4 *>(dst + c * kLanes * kN) = out;
         }
-        *reinterpret_cast<uint4 *>((T *)(i ? a.v_out : a.k_out) + (int64_t)item * D + l0) = Vec<T>::put(x);
       }
     }
   }
@@ -539,7 +557,7 @@ cudaError_t read_go(ReadArgs a, cudaStream_t s) {
   a.by_p = FastDiv(a.P);
   a.by_kv = FastDiv(a.kv);
   a.by_b = FastDiv(a.B);
-  const int64_t threads = (int64_t)a.layers * a.B * a.kv * a.P * (D / Vec<T>::kN);
+  const int64_t threads = (int64_t)a.layers * a.B * a.kv * a.P * (D / Vec<T>::kN / 2);
   const int64_t blocks = (threads + 255) / 256;
   return launch_pdl(k_cache_read<T, Pool, D>, dim3((unsigned)(blocks < 148 * 16 ? blocks : 148 * 16)), 256, 0, s, a);
 }
