@@ -66,7 +66,9 @@ struct RowArgs {
   int per;                     // heads of a token that one lane group rotates
   uint32_t q_blocks;           // blocks of q rows, before those of k (and v) rows
   FastDiv by_q, by_k, by_t;    // by a token's items of q and of k, by T
-  uint64_t turn[128];          // pair i turns by pos * turn[i] * 2^-64 of a full turn
+  // pair i turns by pos * f_i of a full turn, f_i = base^(-2i/D) / 2 pi as a 64-bit fraction:
+  // 1 / 2 pi times ratio[k] = base^(-2 * 2^k / D) for every bit k of i
+  uint64_t ratio[7];
 };
 cudaError_t launch_rows(const RowArgs &a, int dtype, int pool_dtype, int head_dim, cudaStream_t s);
 

@@ -41,20 +41,21 @@ bool rotation_ok(const pi0x_rotation *r) {
          (r->rope_base == 0.0f || (r->rope_base >= 1.0f && isfinite(r->rope_base)));
 }
 
-// Pair i turns by pos * base^(-2i/D) radians: as a 64-bit fraction of a full turn.  A
-// row of fractions depends on (base, D) alone; the last one formed is kept per thread.
-void set_turns(RowArgs &a, float base, int head_dim) {
+// The ratios of a rotation's angles (RowArgs) as 64-bit fractions; one of 1 is a step below it.
+// They depend on (base, D) alone; the last ones formed are kept per thread.
+void set_ratios(RowArgs &a, float base, int head_dim) {
   static thread_local float last_base = 0.0f;
   static thread_local int last_dim = 0;
-  static thread_local uint64_t turn[128];
+  static thread_local uint64_t ratio[7];
   if (base != last_base || head_dim != last_dim) {
-    const long double full = 6.283185307179586476925286766559L;
-    for (int i = 0; i < head_dim / 2; ++i)
-      turn[i] = (uint64_t)(powl((long double)base, -2.0L * i / head_dim) / full * 18446744073709551616.0L);
+    for (int k = 0; k < 7; ++k) {
+      const long double r = powl((long double)base, -2.0L * (1 << k) / head_dim) * 18446744073709551616.0L;
+      ratio[k] = r >= 18446744073709551615.0L ? UINT64_MAX : (uint64_t)r;
+    }
     last_base = base;
     last_dim = head_dim;
   }
-  for (int i = 0; i < head_dim / 2; ++i) a.turn[i] = turn[i];
+  for (int k = 0; k < 7; ++k) a.ratio[k] = ratio[k];
 }
 
 // The norms and the rotation of a RowArgs whose heads are set.
@@ -64,7 +65,7 @@ void set_rotation(RowArgs &a, const pi0x_rotation *rot, int head_dim) {
   a.eps = rot->eps;
   a.positions = rot->positions;
   a.rotate = rot->rope_base > 0.0f;
-  if (a.rotate) set_turns(a, rot->rope_base, head_dim);
+  if (a.rotate) set_ratios(a, rot->rope_base, head_dim);
 }
 
 }  // namespace

@@ -135,6 +135,16 @@ struct PoolInt8 {
   }
 };
 
+// f_i of RowArgs.  A product loses less than a unit, so the angle of a 32-bit position is still
+// exact to 2^-32 of a turn.  (A table of them in the parameters, which lanes index apart, is read
+// one lane after another.)
+__device__ __forceinline__ uint64_t turn_of(const RowArgs &a, int i) {
+  uint64_t f = 2935890503282001226ull;  // 2^64 / 2 pi
+#pragma unroll
+  for (int k = 0; k < 7; ++k)
+    if (i >> k & 1) f = __umul64hi(f, a.ratio[k]);
+  return f;
+}
 // cos and sin of 2 pi t, t = `turn` * 2^-32 of a full turn.  The integer is split into
 // the nearest quarter turn and a rest of at most an eighth (|y| <= pi/4), where the
 // Taylor polynomials of degree 9 and 10 are within 2e-9 and 2e-10.
@@ -307,7 +317,7 @@ template <typename T, typename Pool, int D, bool kTurned, bool kPages>
 __global__ void __launch_bounds__(256, kTurned ? 3 : 4) k_rows(const __grid_constant__ RowArgs a) {
   using M = RowMath<T, D, sizeof(T) == 4 || Pool::kScaled>;
   constexpr int kN = M::kN, kP = M::kP, kLanes = M::kLanes, kGroups = 256 / kLanes, kAhead = kTurned ? 3 : 2;
-  __shared__ uint64_t sm_turn[D / 2];  // lanes index it apart: from the parameters that would be one after another
+  __shared__ uint64_t sm_turn[D / 2];
   __shared__ __align__(16) float sm_gain[D];  // 1 + gain (in 64 bits: the gain)
   pdl_wait();
   pdl_trigger();
@@ -350,7 +360,7 @@ __global__ void __launch_bounds__(256, kTurned ? 3 : 4) k_rows(const __grid_cons
   const int64_t pos = a.positions && kept ? (int64_t)a.positions[tok] : slot;
   const int cell = to_pages && kept ? cache_row(a.pt, b, slot) : -1;  // row of the pools
   if (a.rotate)
-    for (int i = threadIdx.x; i < D / 2; i += 256) sm_turn[M::turn_at(i)] = a.turn[i];
+    for (int i = threadIdx.x; i < D / 2; i += 256) sm_turn[M::turn_at(i)] = turn_of(a, i);
   if (gain)
     for (int i = threadIdx.x; i < D; i += 256)
       sm_gain[M::gain_at(i)] = Pool::kDouble && to_pages ? gain[i] : 1.0f + gain[i];
