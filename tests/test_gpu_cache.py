@@ -430,6 +430,9 @@ def check_attend(c, layer, q, table, lens, mask, scale, out, lse):
     (400, 8, 1, 256, 16, [i * 37 % 701 for i in range(400)]),        # more units than CTAs, evenly split and joined
     (6, 12, 2, 128, 64, [9000, 0, 1, 30000, 17000, 64]),            # a few long ones: units over many CTAs
     (33, 3, 3, 256, 32, [i * 53 % 2000 for i in range(33)]),
+    (3, 20, 2, 256, 16, [6000, 77, 9001]),                          # more than 8 query heads a kv head
+    (2, 48, 2, 128, 64, [15000, 3]),
+    (90, 16, 1, 64, 8, [i * 31 % 400 for i in range(90)]),
 ])
 def test_attend_matches_the_formula(pool, B, H, kv, D, ps, lens):
     g = rng(sum(lens) % 1000 + D)

@@ -25,12 +25,12 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 namespace pi0x {
 
 namespace {
 constexpr int kWarps = 4;
-constexpr int kHeadsPerUnit = 8;  // query heads of one kv head that share a pass: the product's columns
 constexpr int kJoinThreads = 512;
 constexpr float kWeightBits = 15.0f;
 constexpr int kMaxCluster = 8, kClusterBlocks = 16;
@@ -140,27 +140,31 @@ struct CodeInt8 : Code8 {
   }
 };
 
-// Shapes of a (code type, head_dim) variant.
-template <typename C, int D>
+// Shapes of a variant: code type, head_dim, and how many products of 8 columns a unit has (1, or 2
+// where a kv head has more than 8 query heads: keys and values are then read and converted
+// once for 16; 8 x 10k-20k int8 keys of 128 dims, 20 heads on 2: 31 -> 26 us).
+template <typename C, int D, int NT>
 struct Shape {
+  static constexpr int kHeads = 8 * NT;  // query heads of one kv head that share a pass
   static constexpr int kRowBytes = D * C::kBytes;
   static constexpr int kPitch = kRowBytes + 16;  // 8 rows of a matrix fall into different banks
-  // keys a warp takes at once: 16 per product, more where rows are short, so that a buffer
-  // holds 8 KB (4 KB at 64 bytes a row)
-  static constexpr int kTiles = kRowBytes >= 512 ? 1 : 2;
+  // keys a warp takes at once: 16 per product, 32 where rows are short and registers allow it
+  // (64 at 128-byte rows with two blocks an SM instead of three: 54 against 48 us for 24 ragged
+  // int8 samples)
+  static constexpr int kTiles = kRowBytes >= 512 || NT * D >= 512 ? 1 : 2;
   static constexpr int kKeys = 16 * kTiles;
   static constexpr int kBlock = kWarps * kKeys;  // keys of a scheduling block
   static constexpr int kMTiles = D / 16;
   static constexpr int kBuf = kKeys * kPitch;    // bytes of a buffer
-  static constexpr int kRing = 3 * kBuf;
   static constexpr int kHeadPitch = D + 4;       // floats: the warps' sums on their way to each other
-  static_assert(kHeadsPerUnit * kHeadPitch * 4 <= kRing, "a warp's sums fit its ring");
+  static constexpr int kSums = kHeads * kHeadPitch * 4;
+  static constexpr int kRing = 3 * kBuf > kSums ? 3 * kBuf : kSums;  // a warp's sums take its ring
   static constexpr int kSmem = kWarps * kRing;
-  static constexpr int kBlocksPerSm = kRowBytes >= 256 ? 2 : 3;
+  static constexpr int kBlocksPerSm = kRowBytes >= 256 || NT * D >= 256 ? 2 : 3;  // registers allow no more
   static constexpr int kGrid = 148 * kBlocksPerSm;
 };
 
-// Work: units u = (sample, kv head, group of up to 8 query heads), each of ceil(len/kBlock)
+// Work: units u = (sample, kv head, group of up to 8 or 16 query heads), each of ceil(len/kBlock)
 // blocks of keys (at least one).  Two ways to share them out:
 //  * kCluster: a cluster of 1 to 8 CTAs takes a unit, its CTAs in turn a block each, and adds
 //    up the CTAs' sums through distributed shared memory.  One launch, no workspace, and a CTA
@@ -199,27 +203,27 @@ __device__ __forceinline__ int keys_of(const AttendArgs &a, int b) {
   if (a.mask) n = min(n, (int64_t)a.mask_len);
   return n > 0 ? (int)n : 0;
 }
-__host__ __device__ inline int head_groups(int heads, int kv) { return (heads / kv + kHeadsPerUnit - 1) / kHeadsPerUnit; }
-// Floats of a part: 8 heads' sums, then their m and l.
-template <int D>
-constexpr int kPartFloats = kHeadsPerUnit * D + 2 * kHeadsPerUnit;
+__host__ __device__ inline int head_groups(int heads, int kv, int per) { return (heads / kv + per - 1) / per; }
+// Floats of a part: the heads' sums, then their m and l.
+template <int D, int NT>
+constexpr int kPartFloats = 8 * NT * (D + 2);
 
 }  // namespace
 
-template <typename C, int D, bool kCluster>
-__global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
+template <typename C, int D, int NT, bool kCluster>
+__global__ void __launch_bounds__(kWarps * 32, Shape<C, D, NT>::kBlocksPerSm)
     k_attend(const __grid_constant__ AttendArgs a, int cluster) {
-  using S = Shape<C, D>;
+  using S = Shape<C, D, NT>;
   pdl_wait();
   pdl_trigger();
   extern __shared__ __align__(16) uint8_t sm_ring[];
-  __shared__ __align__(16) uint8_t sm_q[kHeadsPerUnit][D * 2 + 16];
-  __shared__ float sm_m[kWarps][kHeadsPerUnit], sm_l[kWarps][kHeadsPerUnit], sm_qf[kHeadsPerUnit];
-  __shared__ float2 sm_ml[kHeadsPerUnit];  // kCluster: this CTA's m and l
+  __shared__ __align__(16) uint8_t sm_q[S::kHeads][D * 2 + 16];
+  __shared__ float sm_m[kWarps][S::kHeads], sm_l[kWarps][S::kHeads], sm_qf[S::kHeads];
+  __shared__ float2 sm_ml[S::kHeads];  // kCluster: this CTA's m and l
   __shared__ int64_t sm_at;
   __shared__ int sm_scan[kWarps], sm_b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int group = a.heads / a.kv, groups = head_groups(a.heads, a.kv), upb = a.kv * groups;
+  const int group = a.heads / a.kv, groups = head_groups(a.heads, a.kv, S::kHeads), upb = a.kv * groups;
   auto blocks_of = [](int len) { return max(1, (int)(((uint32_t)len + S::kBlock - 1) / S::kBlock)); };
 
   // ---- this CTA's blocks [c0, c1), its first sample, and where in the sample's units it starts
@@ -307,8 +311,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
       key_0 = blk0 * S::kBlock + warp * S::kKeys;
       look_end = key_end = (int)min((int64_t)len, ((int64_t)blk0 + nseg) * S::kBlock);
     }
-    const int h = ub / groups, h0 = h * group + (ub % groups) * kHeadsPerUnit;
-    const int nh = min(kHeadsPerUnit, group - (ub % groups) * kHeadsPerUnit);
+    const int h = ub / groups, h0 = h * group + (ub % groups) * S::kHeads;
+    const int nh = min(S::kHeads, group - (ub % groups) * S::kHeads);
 
     // look() issues the loads of a step's page numbers and mask, settle(), a step later, takes
     // what came.  Unseen keys are not read: their rows are filled with zeros.
@@ -331,9 +335,10 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
 
     // q: 16 threads a head.  fp16 products take q times a power of two (so that the largest
     // element is in [1, 2)): exact for all that matters of a bf16 q.
-    {
+#pragma unroll
+    for (int n = tid >> 4; n < S::kHeads; n += kWarps * 2) {
       constexpr int E = D / 16;
-      const int n = tid >> 4, e0 = (tid & 15) * E;
+      const int e0 = (tid & 15) * E;
       uint32_t w[E / 2];
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) w[i] = 0;
@@ -366,24 +371,51 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
     }
     __syncthreads();
 
-    const float qf0 = sm_qf[2 * t], qf1 = sm_qf[2 * t + 1];
-    uint32_t qb[S::kMTiles][2];  // Q^T: column (head) g, in the order in which a lane's keys come
+    // Q^T: column (head) 8 nt + g, in the order in which a lane's keys come; in registers where
+    // they have room for it.
+    constexpr bool kHoldQ = NT * D <= 256;
+    auto read_q = [&](int nt, int i, uint32_t (&r)[2]) {
+      const uint8_t *p = &sm_q[8 * nt + g][32 * i + (C::kScaled ? 8 : 4) * t];
+      r[0] = *reinterpret_cast<const uint32_t *>(p);
+      r[1] = *reinterpret_cast<const uint32_t *>(p + (C::kScaled ? 4 : 16));
+    };
+    uint32_t qb[kHoldQ ? NT : 1][kHoldQ ? S::kMTiles : 1][2];
+    float qf[NT][2];
 #pragma unroll
-    for (int i = 0; i < S::kMTiles; ++i) {
-      const uint8_t *p = &sm_q[g][32 * i + (C::kScaled ? 8 : 4) * t];
-      qb[i][0] = *reinterpret_cast<const uint32_t *>(p);
-      qb[i][1] = *reinterpret_cast<const uint32_t *>(p + (C::kScaled ? 4 : 16));
+    for (int nt = 0; nt < NT; ++nt) {
+      qf[nt][0] = sm_qf[8 * nt + 2 * t], qf[nt][1] = sm_qf[8 * nt + 2 * t + 1];
+      if constexpr (kHoldQ)
+#pragma unroll
+        for (int i = 0; i < S::kMTiles; ++i) read_q(nt, i, qb[nt][i]);
     }
+    // Product i of the scores: 16 keys and 16 dims against every 8 heads.
+    auto score = [&](float (&x)[NT][4], int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (kHoldQ) {
+          C::mma(x[nt], a0, a1, a2, a3, qb[nt][i][0], qb[nt][i][1]);
+        } else {
+          uint32_t q[2];
+          read_q(nt, i, q);
+          C::mma(x[nt], a0, a1, a2, a3, q[0], q[1]);
+        }
+      }
+    };
 
     const uint32_t row_bytes = (uint32_t)a.kv * S::kRowBytes;
     const uint8_t *kbase = (const uint8_t *)a.kp.codes + (int64_t)h * S::kRowBytes;
     const uint8_t *vbase = (const uint8_t *)a.vp.codes + (int64_t)h * S::kRowBytes;
 
-    float o[S::kMTiles][4];
+    float o[NT][S::kMTiles][4];
+    float m[NT][2], l[NT][2];  // of the lane's two columns of every product
+    float w[NT][2];            // 8-bit codes: running maximum of s + log2(value scale) - 15
 #pragma unroll
-    for (int i = 0; i < S::kMTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-    float w0 = -INFINITY, w1 = -INFINITY;  // 8-bit codes: running maximum of s + log2(value scale) - 15
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < S::kMTiles; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
+      m[nt][0] = m[nt][1] = w[nt][0] = w[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
+    }
 
     auto settle = [&](const Look<kRegs> &k, int key) {
       Step<kRegs> st;
@@ -434,10 +466,10 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
       cp_async_wait<2>();
       __syncwarp();
       // S^T = K Q^T: rows (keys) g and g + 8, columns (heads) 2t and 2t + 1
-      float s[S::kTiles][4];
+      float s[NT][S::kTiles][4];
 #pragma unroll
       for (int u = 0; u < S::kTiles; ++u) {
-        float x[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};  // two chains
+        float x[2][NT][4] = {};  // two chains
         const uint32_t at_k = ring + kbuf * S::kBuf + (u * 16 + lane % 16) * S::kPitch + lane / 16 * 16;
 #pragma unroll
         for (int i = 0; i < S::kRowBytes / 32; ++i) {
@@ -447,23 +479,27 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
             uint32_t a0, a1, a2, a3;
             C::halves(r[0], a0, a2);
             C::halves(r[1], a1, a3);
-            C::mma(x[0], a0, a1, a2, a3, qb[2 * i][0], qb[2 * i][1]);
+            score(x[0], 2 * i, a0, a1, a2, a3);
             C::halves(r[2], a0, a2);
             C::halves(r[3], a1, a3);
-            C::mma(x[1], a0, a1, a2, a3, qb[2 * i + 1][0], qb[2 * i + 1][1]);
+            score(x[1], 2 * i + 1, a0, a1, a2, a3);
           } else {
-            C::mma(x[i & 1], r[0], r[1], r[2], r[3], qb[i][0], qb[i][1]);
+            score(x[i & 1], i, r[0], r[1], r[2], r[3]);
           }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[u][i] = (x[0][i] + x[1][i]) * ((i & 1) ? qf1 : qf0);
-        if constexpr (C::kScaled) {
-          const float ka = of_key(now.ks, u, g), kb = of_key(now.ks, u, 8 + g);
-          s[u][0] *= ka, s[u][1] *= ka, s[u][2] *= kb, s[u][3] *= kb;
-        }
+        float ka = 1.0f, kb = 1.0f;
+        if constexpr (C::kScaled) ka = of_key(now.ks, u, g), kb = of_key(now.ks, u, 8 + g);
         const unsigned seen = now.seen[(u * 16) / 32] >> ((u * 16) % 32 + g);
-        if (!(seen & 1)) s[u][0] = s[u][1] = -INFINITY;
-        if (!(seen >> 8 & 1)) s[u][2] = s[u][3] = -INFINITY;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s[nt][u][i] = (x[0][nt][i] + x[1][nt][i]) * qf[nt][i & 1];
+            if constexpr (C::kScaled) s[nt][u][i] *= i < 2 ? ka : kb;
+          }
+          if (!(seen & 1)) s[nt][u][0] = s[nt][u][1] = -INFINITY;
+          if (!(seen >> 8 & 1)) s[nt][u][2] = s[nt][u][3] = -INFINITY;
+        }
       }
       __syncwarp();
       if (key + hop < key_end) copy(next, vbase, kbuf);  // the next step's V takes K's buffer
@@ -471,61 +507,67 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
       const int vbuf = next_buf(kbuf);
 
       // online softmax: columns are heads, so a lane's two factors serve its scores and its sums
-      float n0 = m0, n1 = m1;
-#pragma unroll
-      for (int u = 0; u < S::kTiles; ++u) {
-        n0 = fmaxf(n0, fmaxf(s[u][0], s[u][2]));
-        n1 = fmaxf(n1, fmaxf(s[u][1], s[u][3]));
-      }
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) {
-        n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, d));
-        n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, d));
-      }
-      const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
-      float f0 = ex2_approx(m0 - z0), f1 = ex2_approx(m1 - z1);
-      l0 *= f0, l1 *= f1;
-      m0 = n0, m1 = n1;
-      float p[S::kTiles][4];
-#pragma unroll
-      for (int u = 0; u < S::kTiles; ++u) {
-        p[u][0] = ex2_approx(s[u][0] - z0), p[u][2] = ex2_approx(s[u][2] - z0);
-        p[u][1] = ex2_approx(s[u][1] - z1), p[u][3] = ex2_approx(s[u][3] - z1);
-        l0 += p[u][0] + p[u][2];
-        l1 += p[u][1] + p[u][3];
-      }
-      if constexpr (C::kScaled) {
-        // A value's scale goes into its weight: 2^(s + log2 scale - w + 15) with a maximum w of
-        // its own, which keeps the fp16 weights in range whatever the scales are: the largest is
-        // 2^15, and one of 2^-29 of it still has all 11 bits.
-        float e0 = w0 + kWeightBits, e1 = w1 + kWeightBits, lv[kRegs];
+      float p[NT][S::kTiles][4];
+      float lv[kRegs];
+      if constexpr (C::kScaled)
 #pragma unroll
         for (int r = 0; r < kRegs; ++r) lv[r] = log2_approx(now.vs[r]);
 #pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float n0 = m[nt][0], n1 = m[nt][1];
+#pragma unroll
         for (int u = 0; u < S::kTiles; ++u) {
-          const float va = of_key(lv, u, g), vb = of_key(lv, u, 8 + g);
-          s[u][0] += va, s[u][1] += va, s[u][2] += vb, s[u][3] += vb;
-          e0 = fmaxf(e0, fmaxf(s[u][0], s[u][2]));
-          e1 = fmaxf(e1, fmaxf(s[u][1], s[u][3]));
+          n0 = fmaxf(n0, fmaxf(s[nt][u][0], s[nt][u][2]));
+          n1 = fmaxf(n1, fmaxf(s[nt][u][1], s[nt][u][3]));
         }
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) {
-          e0 = fmaxf(e0, __shfl_xor_sync(kFull, e0, d));
-          e1 = fmaxf(e1, __shfl_xor_sync(kFull, e1, d));
+          n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, d));
+          n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, d));
         }
-        e0 -= kWeightBits, e1 -= kWeightBits;
-        const float y0 = e0 == -INFINITY ? 0.0f : e0, y1 = e1 == -INFINITY ? 0.0f : e1;
-        f0 = ex2_approx(w0 - y0), f1 = ex2_approx(w1 - y1);
-        w0 = e0, w1 = e1;
+        const float z0 = n0 == -INFINITY ? 0.0f : n0, z1 = n1 == -INFINITY ? 0.0f : n1;
+        float f0 = ex2_approx(m[nt][0] - z0), f1 = ex2_approx(m[nt][1] - z1);
+        l[nt][0] *= f0, l[nt][1] *= f1;
+        m[nt][0] = n0, m[nt][1] = n1;
 #pragma unroll
         for (int u = 0; u < S::kTiles; ++u) {
-          p[u][0] = ex2_approx(s[u][0] - y0), p[u][2] = ex2_approx(s[u][2] - y0);
-          p[u][1] = ex2_approx(s[u][1] - y1), p[u][3] = ex2_approx(s[u][3] - y1);
+          p[nt][u][0] = ex2_approx(s[nt][u][0] - z0), p[nt][u][2] = ex2_approx(s[nt][u][2] - z0);
+          p[nt][u][1] = ex2_approx(s[nt][u][1] - z1), p[nt][u][3] = ex2_approx(s[nt][u][3] - z1);
+          l[nt][0] += p[nt][u][0] + p[nt][u][2];
+          l[nt][1] += p[nt][u][1] + p[nt][u][3];
         }
-      }
-      if (__any_sync(kFull, !(f0 == 1.0f && f1 == 1.0f))) {
+        if constexpr (C::kScaled) {
+          // A value's scale goes into its weight: 2^(s + log2 scale - w + 15) with a maximum w of
+          // its own, which keeps the fp16 weights in range whatever the scales are: the largest is
+          // 2^15, and one of 2^-29 of it still has all 11 bits.
+          float e0 = w[nt][0] + kWeightBits, e1 = w[nt][1] + kWeightBits;
 #pragma unroll
-        for (int i = 0; i < S::kMTiles; ++i) o[i][0] *= f0, o[i][1] *= f1, o[i][2] *= f0, o[i][3] *= f1;
+          for (int u = 0; u < S::kTiles; ++u) {
+            const float va = of_key(lv, u, g), vb = of_key(lv, u, 8 + g);
+            s[nt][u][0] += va, s[nt][u][1] += va, s[nt][u][2] += vb, s[nt][u][3] += vb;
+            e0 = fmaxf(e0, fmaxf(s[nt][u][0], s[nt][u][2]));
+            e1 = fmaxf(e1, fmaxf(s[nt][u][1], s[nt][u][3]));
+          }
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) {
+            e0 = fmaxf(e0, __shfl_xor_sync(kFull, e0, d));
+            e1 = fmaxf(e1, __shfl_xor_sync(kFull, e1, d));
+          }
+          e0 -= kWeightBits, e1 -= kWeightBits;
+          const float y0 = e0 == -INFINITY ? 0.0f : e0, y1 = e1 == -INFINITY ? 0.0f : e1;
+          f0 = ex2_approx(w[nt][0] - y0), f1 = ex2_approx(w[nt][1] - y1);
+          w[nt][0] = e0, w[nt][1] = e1;
+#pragma unroll
+          for (int u = 0; u < S::kTiles; ++u) {
+            p[nt][u][0] = ex2_approx(s[nt][u][0] - y0), p[nt][u][2] = ex2_approx(s[nt][u][2] - y0);
+            p[nt][u][1] = ex2_approx(s[nt][u][1] - y1), p[nt][u][3] = ex2_approx(s[nt][u][3] - y1);
+          }
+        }
+        if (__any_sync(kFull, !(f0 == 1.0f && f1 == 1.0f))) {
+#pragma unroll
+          for (int i = 0; i < S::kMTiles; ++i)
+            o[nt][i][0] *= f0, o[nt][i][1] *= f1, o[nt][i][2] *= f0, o[nt][i][3] *= f1;
+        }
       }
 
       // O^T += V^T P^T: rows are dims (16i + g and 16i + 8 + g in bf16, 16i + 2g and + 1 of 8-bit codes)
@@ -533,8 +575,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
       __syncwarp();
 #pragma unroll
       for (int u = 0; u < S::kTiles; ++u) {
-        const uint32_t b0 = transpose8x8(C::pack(p[u][0], p[u][1]));
-        const uint32_t b1 = transpose8x8(C::pack(p[u][2], p[u][3]));
+        uint32_t b0[NT], b1[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          b0[nt] = transpose8x8(C::pack(p[nt][u][0], p[nt][u][1]));
+          b1[nt] = transpose8x8(C::pack(p[nt][u][2], p[nt][u][3]));
+        }
         const int half = lane / 16, odd = lane / 8 % 2;  // bf16: keys, dims; 8-bit codes: dims, keys
         const uint32_t at_v = ring + vbuf * S::kBuf + (u * 16 + (C::kScaled ? odd : half) * 8 + lane % 8) * S::kPitch +
                               (C::kScaled ? half : odd) * 16;
@@ -547,12 +593,15 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
             uint32_t a0, a1, a2, a3;
             C::halves(prmt(r[0], 0, 0x3120), a0, a1);
             C::halves(prmt(r[1], 0, 0x3120), a2, a3);
-            C::mma(o[2 * i], a0, a1, a2, a3, b0, b1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) C::mma(o[nt][2 * i], a0, a1, a2, a3, b0[nt], b1[nt]);
             C::halves(prmt(r[2], 0, 0x3120), a0, a1);
             C::halves(prmt(r[3], 0, 0x3120), a2, a3);
-            C::mma(o[2 * i + 1], a0, a1, a2, a3, b0, b1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) C::mma(o[nt][2 * i + 1], a0, a1, a2, a3, b0[nt], b1[nt]);
           } else {
-            C::mma(o[i], r[0], r[1], r[2], r[3], b0, b1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) C::mma(o[nt][i], r[0], r[1], r[2], r[3], b0[nt], b1[nt]);
           }
         }
       }
@@ -566,39 +615,43 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
     }
 
     // ---- the warps' sums together
-#pragma unroll
-    for (int d = 4; d < 32; d <<= 1) {
-      l0 += __shfl_xor_sync(kFull, l0, d);
-      l1 += __shfl_xor_sync(kFull, l1, d);
-    }
-    if constexpr (C::kScaled) {  // from the weights' maximum back to the scores'
-      const float f0 = m0 == -INFINITY || w0 == -INFINITY ? 0.0f : ex2_approx(w0 - m0);
-      const float f1 = m1 == -INFINITY || w1 == -INFINITY ? 0.0f : ex2_approx(w1 - m1);
-#pragma unroll
-      for (int i = 0; i < S::kMTiles; ++i) o[i][0] *= f0, o[i][1] *= f1, o[i][2] *= f0, o[i][3] *= f1;
-    }
-    if (g == 0) {
-      sm_m[warp][2 * t] = m0, sm_m[warp][2 * t + 1] = m1;
-      sm_l[warp][2 * t] = l0, sm_l[warp][2 * t + 1] = l1;
-    }
     cp_async_wait<0>();  // the ring is empty: its first bytes take this warp's sums
     __syncwarp();
     float *mine_o = reinterpret_cast<float *>(sm_ring + warp * S::kRing);
 #pragma unroll
-    for (int i = 0; i < S::kMTiles; ++i) {
-      float *p0 = mine_o + 2 * t * S::kHeadPitch + 16 * i + (C::kScaled ? 2 : 1) * g, *p1 = p0 + S::kHeadPitch;
-      if constexpr (C::kScaled) {
-        *reinterpret_cast<float2 *>(p0) = make_float2(o[i][0], o[i][2]);
-        *reinterpret_cast<float2 *>(p1) = make_float2(o[i][1], o[i][3]);
-      } else {
-        p0[0] = o[i][0], p0[8] = o[i][2];
-        p1[0] = o[i][1], p1[8] = o[i][3];
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) {
+        l[nt][0] += __shfl_xor_sync(kFull, l[nt][0], d);
+        l[nt][1] += __shfl_xor_sync(kFull, l[nt][1], d);
+      }
+      const int n = 8 * nt + 2 * t;
+      if (g == 0) {
+        sm_m[warp][n] = m[nt][0], sm_m[warp][n + 1] = m[nt][1];
+        sm_l[warp][n] = l[nt][0], sm_l[warp][n + 1] = l[nt][1];
+      }
+      float f0 = 1.0f, f1 = 1.0f;
+      if constexpr (C::kScaled) {  // from the weights' maximum back to the scores'
+        f0 = m[nt][0] == -INFINITY || w[nt][0] == -INFINITY ? 0.0f : ex2_approx(w[nt][0] - m[nt][0]);
+        f1 = m[nt][1] == -INFINITY || w[nt][1] == -INFINITY ? 0.0f : ex2_approx(w[nt][1] - m[nt][1]);
+      }
+#pragma unroll
+      for (int i = 0; i < S::kMTiles; ++i) {
+        const float(&x)[4] = o[nt][i];
+        float *p0 = mine_o + n * S::kHeadPitch + 16 * i + (C::kScaled ? 2 : 1) * g, *p1 = p0 + S::kHeadPitch;
+        if constexpr (C::kScaled) {
+          *reinterpret_cast<float2 *>(p0) = make_float2(x[0] * f0, x[2] * f0);
+          *reinterpret_cast<float2 *>(p1) = make_float2(x[1] * f1, x[3] * f1);
+        } else {
+          p0[0] = x[0], p0[8] = x[2];
+          p1[0] = x[1], p1[8] = x[3];
+        }
       }
     }
     __syncthreads();
     const bool whole = kCluster ? cluster == 1 : nseg == nblk;
     const int slot = 2 * (int)blockIdx.x + (c > c0);
-    float *part = parts + (int64_t)slot * kPartFloats<D>;
+    float *part = parts + (int64_t)slot * kPartFloats<D, NT>;
     auto finish = [&](int n, int d, const float4 &x, float m, float l) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const int64_t at_out = ((int64_t)b * a.heads + h0 + n);
@@ -628,7 +681,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
         if (d == 0) sm_ml[n] = make_float2(mm, l);
       } else {
         *reinterpret_cast<float4 *>(part + n * D + d) = x;
-        if (d == 0) part[kHeadsPerUnit * D + 2 * n] = mm, part[kHeadsPerUnit * D + 2 * n + 1] = l;
+        if (d == 0) part[S::kHeads * D + 2 * n] = mm, part[S::kHeads * D + 2 * n + 1] = l;
       }
     }
     if constexpr (kCluster) {
@@ -681,27 +734,27 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D>::kBlocksPerSm)
   }
 }
 
-// Adds up the parts of split unit blockIdx.x, in order of the keys.  A part is 8 heads x D/4
+// Adds up the parts of split unit blockIdx.x, in order of the keys.  A part is 8 NT heads x D/4
 // vectors; blockIdx.y takes an equal share of them, so that a few units with hundreds of
 // parts spread over many SMs.  A share's vectors take `lanes` threads, and the block's groups
 // of so many threads take turns at the parts, each with a running maximum of its own, so that
 // one barrier is enough.  Bound by the L2's latency: kAhead parts are loaded at once.
-template <int D>
+template <int D, int NT>
 __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_constant__ AttendArgs a, int grid) {
   pdl_wait();
   pdl_trigger();
-  constexpr int kAhead = 8, kStats = kHeadsPerUnit * D;
+  constexpr int kAhead = 8, kStats = 8 * NT * D;
   __shared__ float4 sm_x[kJoinThreads];
   __shared__ float2 sm_ml[kJoinThreads];
   const Split sp = reinterpret_cast<const Split *>(a.part)[blockIdx.x];
   if (sp.unit < 0) return;
   const float *parts = a.part + grid * (sizeof(Split) / 4);
   const int tid = threadIdx.x;
-  const int group = a.heads / a.kv, groups = head_groups(a.heads, a.kv), upb = a.kv * groups;
-  const int b = sp.unit / upb, ub = sp.unit % upb, h0 = ub / groups * group + ub % groups * kHeadsPerUnit;
-  const int nh = min(kHeadsPerUnit, group - ub % groups * kHeadsPerUnit);
+  const int group = a.heads / a.kv, groups = head_groups(a.heads, a.kv, 8 * NT), upb = a.kv * groups;
+  const int b = sp.unit / upb, ub = sp.unit % upb, h0 = ub / groups * group + ub % groups * 8 * NT;
+  const int nh = min(8 * NT, group - ub % groups * 8 * NT);
   const int count = sp.last - sp.first + 1;
-  const int lanes = 2 * D / gridDim.y, turns = kJoinThreads / lanes, turn = tid / lanes;  // 4 <= lanes <= kJoinThreads
+  const int lanes = 2 * NT * D / gridDim.y, turns = kJoinThreads / lanes, turn = tid / lanes;  // 4 <= lanes <= kJoinThreads
   const int v = blockIdx.y * lanes + tid % lanes, head = v / (D / 4);
   const bool mine = head < nh;
 
@@ -721,7 +774,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
     for (int q = 0; q < kAhead; ++q) {
       const int j = j0 + q * turns;
       if (j < count) {
-        const float *part = parts + (int64_t)(j == 0 ? sp.slot : 2 * (sp.first + j)) * kPartFloats<D>;
+        const float *part = parts + (int64_t)(j == 0 ? sp.slot : 2 * (sp.first + j)) * kPartFloats<D, NT>;
         y[q] = *reinterpret_cast<const float4 *>(part + 4 * v);
         ml[q] = *reinterpret_cast<const float2 *>(part + kStats + 2 * head);
       }
@@ -778,11 +831,11 @@ struct Plan {
   int cluster;  // CTAs of a cluster, 0: even shares and a join
   int grid;
 };
-template <typename C, int D>
+template <typename C, int D, int NT>
 Plan attend_plan(int B, int heads, int kv, int page_size, int max_pages) {
-  using S = Shape<C, D>;
+  using S = Shape<C, D, NT>;
   const int64_t blocks = ((int64_t)page_size * max_pages + S::kBlock - 1) / S::kBlock;
-  const int64_t units = (int64_t)B * kv * head_groups(heads, kv);
+  const int64_t units = (int64_t)B * kv * head_groups(heads, kv, S::kHeads);
   int cluster = 1;
   while (cluster < kMaxCluster && cluster < blocks && units * cluster * 2 <= S::kGrid) cluster *= 2;
   const int64_t even = (units * blocks + S::kGrid - 1) / S::kGrid;
@@ -791,28 +844,29 @@ Plan attend_plan(int B, int heads, int kv, int page_size, int max_pages) {
   if (even <= kClusterBlocks && mine <= even + slack) return Plan{cluster, (int)(units * cluster)};
   return Plan{0, (int)(units * blocks < S::kGrid ? units * blocks : S::kGrid)};
 }
-template <typename C, int D>
+template <typename C, int D, int NT>
 size_t attend_bytes(int B, int heads, int kv, int page_size, int max_pages) {
-  const Plan p = attend_plan<C, D>(B, heads, kv, page_size, max_pages);
-  return p.cluster || p.grid == 1 ? 0 : p.grid * (sizeof(Split) + 2 * kPartFloats<D> * sizeof(float));
+  const Plan p = attend_plan<C, D, NT>(B, heads, kv, page_size, max_pages);
+  return p.cluster || p.grid == 1 ? 0 : p.grid * (sizeof(Split) + 2 * kPartFloats<D, NT> * sizeof(float));
 }
 // Dynamic shared memory beyond 48 KB has to be asked for once a device and kernel.
-template <typename C, int D, bool kCluster>
+template <typename C, int D, int NT, bool kCluster>
 cudaError_t allow_smem() {
   static std::atomic<uint64_t> allowed{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (dev < 64 && allowed.load(std::memory_order_relaxed) >> dev & 1)) return e;
-  e = cudaFuncSetAttribute(k_attend<C, D, kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<C, D>::kSmem);
+  e = cudaFuncSetAttribute(k_attend<C, D, NT, kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Shape<C, D, NT>::kSmem);
   if (e == cudaSuccess && dev < 64) allowed.fetch_or(1ull << dev, std::memory_order_relaxed);
   return e;
 }
-template <typename C, int D>
+template <typename C, int D, int NT>
 cudaError_t attend_go(const AttendArgs &a, cudaStream_t s) {
-  using S = Shape<C, D>;
-  const Plan p = attend_plan<C, D>(a.B, a.heads, a.kv, a.pt.page_size, a.pt.max_pages);
+  using S = Shape<C, D, NT>;
+  const Plan p = attend_plan<C, D, NT>(a.B, a.heads, a.kv, a.pt.page_size, a.pt.max_pages);
   if (p.cluster) {
-    const cudaError_t e = allow_smem<C, D, true>();
+    const cudaError_t e = allow_smem<C, D, NT, true>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.grid);
@@ -827,36 +881,43 @@ cudaError_t attend_go(const AttendArgs &a, cudaStream_t s) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_attend<C, D, true>, a, p.cluster);
+    return cudaLaunchKernelEx(&cfg, k_attend<C, D, NT, true>, a, p.cluster);
   }
-  cudaError_t e = allow_smem<C, D, false>();
-  if (e == cudaSuccess) e = launch_pdl(k_attend<C, D, false>, dim3(p.grid), kWarps * 32, S::kSmem, s, a, 0);
+  cudaError_t e = allow_smem<C, D, NT, false>();
+  if (e == cudaSuccess) e = launch_pdl(k_attend<C, D, NT, false>, dim3(p.grid), kWarps * 32, S::kSmem, s, a, 0);
   if (e != cudaSuccess || p.grid == 1) return e;  // one CTA: nothing is split
-  const int64_t units = (int64_t)a.B * a.kv * head_groups(a.heads, a.kv);
+  const int64_t units = (int64_t)a.B * a.kv * head_groups(a.heads, a.kv, S::kHeads);
   const int lists = (int)(units < p.grid ? units : p.grid);
   // Shares of a split unit: about one CTA an SM in all, of 16 vectors or more, of 4 where a unit
   // has 128 parts or more (1 x 4096 keys in 64 parts: 8.8 us with 16 vectors, 10.0 with 4;
   // 1 x 32768 in 256: 14.7 and 14.1).
   const int finest = p.grid / lists >= 128 ? D / 2 : D / 8;
-  int shares = 1;
+  int shares = 2 * NT * D / kJoinThreads > 1 ? 2 * NT * D / kJoinThreads : 1;
   while (shares < finest && lists * shares * 2 <= 148) shares *= 2;
-  return launch_pdl(k_attend_join<D>, dim3(lists, shares), kJoinThreads, 0, s, a, p.grid);
+  return launch_pdl(k_attend_join<D, NT>, dim3(lists, shares), kJoinThreads, 0, s, a, p.grid);
 }
 
-#define PI0X_PICK(fn, dtype, dim, ...)                                                                      \
-  auto by_dim = [&](auto c) {                                                                               \
-    using C = decltype(c);                                                                                  \
-    return (dim) == 64 ? fn<C, 64>(__VA_ARGS__) : (dim) == 128 ? fn<C, 128>(__VA_ARGS__) : fn<C, 256>(__VA_ARGS__); \
-  };                                                                                                        \
-  return (dtype) == PI0X_DTYPE_E4M3 ? by_dim(CodeE4m3()) : (dtype) == PI0X_DTYPE_INT8 ? by_dim(CodeInt8()) : by_dim(CodeBf16())
+#define PI0X_PICK(fn, dtype, dim, group, ...)                                                     \
+  auto by_group = [&](auto c, auto d) {                                                           \
+    using C = decltype(c);                                                                        \
+    return (group) > 8 ? fn<C, d(), 2>(__VA_ARGS__) : fn<C, d(), 1>(__VA_ARGS__);                  \
+  };                                                                                              \
+  auto by_dim = [&](auto c) {                                                                     \
+    return (dim) == 64    ? by_group(c, std::integral_constant<int, 64>())                        \
+           : (dim) == 128 ? by_group(c, std::integral_constant<int, 128>())                       \
+                          : by_group(c, std::integral_constant<int, 256>());                      \
+  };                                                                                              \
+  return (dtype) == PI0X_DTYPE_E4M3   ? by_dim(CodeE4m3())                                        \
+         : (dtype) == PI0X_DTYPE_INT8 ? by_dim(CodeInt8())                                        \
+                                      : by_dim(CodeBf16())
 
 }  // namespace
 
 size_t attend_workspace(int B, int heads, int kv, int head_dim, int pool_dtype, int page_size, int max_pages) {
-  PI0X_PICK(attend_bytes, pool_dtype, head_dim, B, heads, kv, page_size, max_pages);
+  PI0X_PICK(attend_bytes, pool_dtype, head_dim, heads / kv, B, heads, kv, page_size, max_pages);
 }
 cudaError_t launch_attend(const AttendArgs &a, int pool_dtype, int head_dim, cudaStream_t s) {
-  PI0X_PICK(attend_go, pool_dtype, head_dim, a, s);
+  PI0X_PICK(attend_go, pool_dtype, head_dim, a.heads / a.kv, a, s);
 }
 
 }  // namespace pi0x
