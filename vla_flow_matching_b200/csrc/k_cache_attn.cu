@@ -49,6 +49,18 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+// cp.async of 16 bytes, or of 16 zero bytes, whose line is the first to leave the L2: keys and values
+// are read once, page numbers, parts and the kernels' own code are wanted again.
+__device__ __forceinline__ uint64_t evict_first() {
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  return policy;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool valid, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src),
+               "r"(valid ? 16 : 0), "l"(policy)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
 // The 8x8 matrix of 16-bit elements spread over the warp, transposed.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
@@ -436,6 +448,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D, NT>::kBlocksPerSm)
       return st;
     };
     const uint32_t ring = smem_u32(sm_ring) + warp * S::kRing;
+    const uint64_t policy = evict_first();
     // A step's rows into a buffer: kRowBytes / 16 lanes a row, consecutive bytes.
     auto copy = [&](const Step<kRegs> &st, const uint8_t *base, int buf) {
       constexpr int kLanes = S::kRowBytes / 16, kAtOnce = 32 / kLanes;
@@ -444,7 +457,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D, NT>::kBlocksPerSm)
 #pragma unroll
       for (int i = 0; i < S::kKeys; i += kAtOnce) {
         const int row = __shfl_sync(kFull, st.rows[i / 32], i % 32 + lane / kLanes);
-        cp_async16(dst + i * S::kPitch, src + (uint64_t)(uint32_t)max(row, 0) * row_bytes, row >= 0);
+        copy16(dst + i * S::kPitch, src + (uint64_t)(uint32_t)max(row, 0) * row_bytes, row >= 0, policy);
       }
     };
     auto next_buf = [](int buf) { return buf == 2 ? 0 : buf + 1; };
