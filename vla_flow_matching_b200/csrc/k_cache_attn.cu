@@ -701,7 +701,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<C, D, NT>::kBlocksPerSm)
       if (whole) return;
       // Vectors of 4 dims in turn over the CTAs.  (Reading every warp's sums of the peers here,
       // without the step above, measured slower: four times the remote bytes, 27 against 23 us
-      // for 128 robots.)
+      // for 128 robots; so did CTAs putting their sums into the shared memory of the one that
+      // adds them up, 12.5 against 9.5 us for 32 robots.)
       cluster_sync();
       for (int i = rank * kWarps * 32 + tid; i < nh * (D / 4); i += cluster * kWarps * 32) {
         const int n = i / (D / 4), d = i % (D / 4) * 4;
@@ -837,9 +838,9 @@ namespace {
 // and values in every CTA.  Clusters where that is the larger cost, and only while the even
 // share is small: with more work the second kernel hardly shows, and ragged samples keep the CTAs
 // of a cluster waiting (lengths are not known here: the page tables' are taken).  GPU time of a
-// call in us, clusters / even shares: 1 x 816 bf16 keys of 256 dims 7.2 / 8.7, 1 x 4096
-// 13.7 / 8.9, 40 x 1000-2000 18.4 / 21.3, 128 x 600-816 22.5 / 26.1, 256 x 600-816 36.7 /
-// 44.5; 512 x 300-700 int8 keys of 64 dims 14.3 / 24.3.
+// call in us, clusters / even shares: 1 x 816 bf16 keys of 256 dims 7.1 / 8.5, 1 x 4096
+// 13.9 / 8.6, 40 x 1000-2000 17.8 / 19.7, 128 x 600-816 21.1 / 23.9, 256 x 600-816 35.4 /
+// 41.0; 512 x 300-700 int8 keys of 64 dims 13.9 / 23.7.
 struct Plan {
   int cluster;  // CTAs of a cluster, 0: even shares and a join
   int grid;
