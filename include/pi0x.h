@@ -144,8 +144,8 @@ int pi0x_sync_status(pi0x_handle *h);
  *
  * Every pointer below is device memory of the current device, of its elements'
  * alignment at least.  The calls enqueue
- * their work on `stream` and return; they allocate nothing, keep nothing, and may be
- * captured into a CUDA graph (pi0x_sample_cache excepted).  What can be seen from the host is checked
+ * their work on `stream` and return; they allocate nothing, keep nothing of a call's data, and
+ * may be captured into a CUDA graph (pi0x_sample_cache excepted).  What can be seen from the host is checked
  * (PI0X_EINVAL, PI0X_EUNSUPPORTED); what lies in device memory is bounded by the
  * kernels: a page table entry outside [0, num_pages) is a page without keys (nothing
  * is read or written there), a length below 0 counts as 0 and one above the table's
@@ -164,7 +164,8 @@ typedef struct {
 } pi0x_cache;
 
 /* Rows of `head_dim` contiguous elements at data + b * batch_stride + t * token_stride
- * + h * head_stride (elements); data and the strides are multiples of 16 bytes. */
+ * + h * head_stride (elements); data and the strides are multiples of 16 bytes.
+ * An input's rows may share memory (strides of 0), an output's may not. */
 typedef struct {
   void *data;
   int64_t batch_stride, token_stride, head_stride;

@@ -115,6 +115,16 @@ def test_qk_norm_rope_refuses(lib, kw, status):
                                  d["rot"], rows(), d["k_out"], None) == status
 
 
+@pytest.mark.parametrize("b,t,h", [(0, 256, 128), (1024, 0, 128), (1024, 256, 0), (1024, 256, 64), (1024, -64, 128)])
+def test_outputs_whose_rows_overlap_are_refused(lib, b, t, h):
+    bad, rot = rows(PTR, b, t, h), Rotation(0, 0, 0, 1e-6, 1e4)
+    assert lib.pi0x_qk_norm_rope(BF16, 2, 2, 2, 0, 128, rows(), None, None, rot, bad, None, None) == EINVAL
+    assert lib.pi0x_qk_norm_rope(BF16, 2, 2, 0, 2, 128, None, rows(), None, rot, None, bad, None) == EINVAL
+    assert lib.pi0x_cache_write(cache(), 0, BF16, 2, 2, rows(), rows(), PTR, 4, PTR, None, rot, 2, rows(), bad,
+                                None) == EINVAL
+    assert b"overlap" in lib.pi0x_last_error()
+
+
 def test_sample_cache_refuses_null_arguments(lib):
     assert lib.pi0x_sample_cache(None, cache(), 1, 8, PTR, 4, PTR, None, PTR, PTR, 1, PTR, None) == EINVAL
     assert lib.pi0x_sample_cache(None, None, 1, 8, None, 0, None, None, None, None, 1, None, None) == EINVAL

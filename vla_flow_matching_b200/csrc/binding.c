@@ -323,7 +323,7 @@ static PyObject *py_qk_norm_rope(PyObject *self, PyObject *const *a, Py_ssize_t 
   if (!qo) return NULL;
   ko = has_k ? out_rows(what, "k_out", a[9], a[1], &k, B, T, kv, D, q.dtype, &rko, &device) : Py_NewRef(Py_None);
   if (!ko) goto out;
-  if (B * T * (heads + kv) != 0) {
+  if (B != 0 && T != 0 && heads + kv != 0) {
     void *stream;
     int st;
     if (current_stream(device, &stream)) goto out;

@@ -33,6 +33,11 @@ bool rows_ok(const pi0x_rows *r, int elem) {
   return r && r->data && aligned(r->data) && r->batch_stride % n == 0 && r->token_stride % n == 0 &&
          r->head_stride % n == 0;
 }
+// An output's rows, `head_dim` elements each, do not share memory with the next ones.
+bool apart(const pi0x_rows *r, int B, int T, int heads, int head_dim) {
+  auto ok = [&](int n, int64_t stride) { return n < 2 || stride >= head_dim || stride <= -head_dim; };
+  return ok(B, r->batch_stride) && ok(T, r->token_stride) && ok(heads, r->head_stride);
+}
 RowsPtr rows_of(const pi0x_rows *r) { return RowsPtr{r->data, r->batch_stride, r->token_stride, r->head_stride}; }
 
 bool rotation_ok(const pi0x_rotation *r) {
@@ -116,6 +121,8 @@ int pi0x_qk_norm_rope(int dtype, int B, int T, int q_heads, int k_heads, int hea
   if ((q_heads && (!rows_ok(q, elem) || !rows_ok(q_out, elem))) ||
       (k_heads && (!rows_ok(k, elem) || !rows_ok(k_out, elem))))
     return refuse(PI0X_EINVAL, "pi0x_qk_norm_rope: rows must be given, with data and strides in whole 16 bytes");
+  if ((q_heads && !apart(q_out, B, T, q_heads, head_dim)) || (k_heads && !apart(k_out, B, T, k_heads, head_dim)))
+    return refuse(PI0X_EINVAL, "pi0x_qk_norm_rope: rows of an output overlap");
   if (!rotation_ok(rot)) return refuse(PI0X_EINVAL, "pi0x_qk_norm_rope: gain alignment, eps or rope_base");
   if ((int64_t)B * T > INT32_MAX / ((int64_t)q_heads + k_heads))
     return refuse(PI0X_EINVAL, "pi0x_qk_norm_rope: 2^31 rows or more");
@@ -144,6 +151,8 @@ int pi0x_cache_write(const pi0x_cache *cache, int layer, int dtype, int B, int T
   const int elem = dtype == PI0X_DTYPE_F32 ? 4 : 2;
   if (!rows_ok(k, elem) || !rows_ok(v, elem) || (q_heads && (!rows_ok(q, elem) || !rows_ok(q_out, elem))))
     return refuse(PI0X_EINVAL, "pi0x_cache_write: rows must be given, with data and strides in whole 16 bytes");
+  if (q_heads && !apart(q_out, B, T, q_heads, cache->head_dim))
+    return refuse(PI0X_EINVAL, "pi0x_cache_write: rows of q_out overlap");
   if (rot && !rotation_ok(rot)) return refuse(PI0X_EINVAL, "pi0x_cache_write: gain alignment, eps or rope_base");
   if ((int64_t)B * T > INT32_MAX / ((int64_t)q_heads + 2 * cache->kv_heads))
     return refuse(PI0X_EINVAL, "pi0x_cache_write: 2^31 rows or more");
