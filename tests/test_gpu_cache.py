@@ -5,7 +5,11 @@ Tolerances count roundings.  An output of type t is off by at most half a step,
 ``finfo(t).eps / 2`` of its value; what is computed in fp32 before that adds its share,
 given at each check.
 """
+import concurrent.futures
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -452,6 +456,18 @@ def test_attend_matches_the_formula(pool, B, H, kv, D, ps, lens):
 
 
 @pytest.mark.parametrize("pool", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("lens", [[5, 0, 70], [0, 0, 0], [1, 130, 2000]])
+def test_attend_of_short_samples_in_a_long_table(pool, lens):
+    g = rng(21)
+    c = make_cache(pool, 1, 40, 64, 2, 128, 22)
+    table = torch.full((3, 4096), -1, device="cuda", dtype=torch.int32)
+    table[:, :32] = torch.randint(0, 40, (3, 32), device="cuda", generator=g, dtype=torch.int32)
+    q, lens = randn(g, 3, 8, 128, dtype=BF16), ints(lens)
+    out, lse = c.attend(0, q, table, lens)
+    check_attend(c, 0, q, table, lens, None, None, out, lse)
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3", "int8"])
 def test_attend_extremes(pool):
     g = rng(4)
     c = make_cache(pool, 1, 40, 16, 1, 128, 3)
@@ -545,6 +561,69 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     for i, (o, l) in enumerate(got):
         assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+
+
+def test_calls_from_several_threads():
+    g = rng(12)
+    caches = [make_cache("int8", 1, 200, 16, 1, 256, 30 + i) for i in range(4)]
+    table, lens = scattered(g, 2, 60, 200), ints([900, 333])
+    q, k, v = (randn(g, 2, 1, h, 256, dtype=BF16) for h in (8, 1, 1))
+    bases = [1e4, 5e5, 1e2, 1e6]
+
+    def step(i):
+        qo = caches[i].write(0, k, v, table, lens - 1, q=q, rope_base=bases[i])
+        return (qo,) + caches[i].attend(0, qo[:, 0], table, lens)
+
+    want = [step(i) for i in range(4)]
+    torch.cuda.synchronize()
+
+    def many(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = [step(i) for _ in range(20)]
+            torch.cuda.current_stream().synchronize()
+        return got
+
+    with concurrent.futures.ThreadPoolExecutor(4) as pool:
+        for i, got in enumerate(pool.map(many, range(4))):
+            for one in got:
+                assert all(torch.equal(x, y) for x, y in zip(one, want[i])), i
+
+
+FIRST_CALLS = """
+import torch
+from vla_flow_matching_b200 import pi0x
+c = pi0x.KVCache.empty(2, 1800, 16, 1, 256, "e4m3")
+q, k, v = (torch.randn(2, 1, h, 256, device="cuda", dtype=torch.bfloat16) for h in (8, 1, 1))
+table = torch.arange(1800, device="cuda", dtype=torch.int32).view(2, 900)
+start = torch.tensor([1900, 3], device="cuda", dtype=torch.int32)
+lens = start + 1
+def step():
+    a, b = pi0x.qk_norm_rope(q, k, start)
+    c.write(0, b, v, table, start)
+    c.write(1, k, v, table, start, q=q, rope_base=10000.0)
+    return (a,) + c.attend(0, a[:, 0], table, lens) + c.attend(0, a[:, 0], table[:, :4].contiguous(), lens) + \
+        c.read(table, lens, 1901)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(x, y) for x, y in zip(got, step()))
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_can_be_captured():
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+def test_the_pools_of_a_cache_stay_its_own():
+    c = pi0x.KVCache.empty(1, 2, 16, 1, 64)
+    for name in ("k", "v", "k_scale", "v_scale"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, c.k)
 
 
 def test_captured_step_follows_its_inputs():

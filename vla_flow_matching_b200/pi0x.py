@@ -261,13 +261,19 @@ class KVCache:
         for t in (k, v, k_scale, v_scale):
             if t is not None and (not t.is_cuda or t.device != k.device):
                 raise ValueError("KVCache: every pool must be on one CUDA device")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._pools = k, v, k_scale, v_scale
         self.layers, self.num_pages, self.page_size, self.kv_heads, self.head_dim = k.shape
         self.device = k.device
         self._index = k.device.index
         self._desc = Cache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), *k.shape, types[k.dtype])
         self._address = ctypes.addressof(self._desc)
         load()
+
+    # The descriptor holds these tensors' addresses, so they stay the cache's for its life.
+    k = property(lambda self: self._pools[0])
+    v = property(lambda self: self._pools[1])
+    k_scale = property(lambda self: self._pools[2])
+    v_scale = property(lambda self: self._pools[3])
 
     @classmethod
     def empty(cls, layers: int, num_pages: int, page_size: int, kv_heads: int = 1, head_dim: int = 256,
