@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -45,9 +46,10 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    made = [LIB] + ([BINDING] if importlib.util.find_spec("torch") else [])
+    if not all(os.path.exists(p) for p in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(p) for p in made)
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -76,8 +78,13 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    # finds libpi0x.so beside itself; Python's own symbols are the interpreter's
+    torch = importlib.util.find_spec("torch")
+    if torch is None:  # the paged-cache calls take torch tensors
+        return LIB
+    # finds libpi0x.so beside itself; Python's own symbols are the interpreter's; of torch only the
+    # DLPack header is used
     cmd = ["gcc", "-O2", "-Wall", "-Wextra", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(torch.submodule_search_locations[0], "include"),
            os.path.join(CSRC, "binding.c"), "-o", BINDING + ".tmp", "-L", PKG, "-l:libpi0x.so", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
