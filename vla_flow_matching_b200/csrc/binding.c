@@ -216,20 +216,29 @@ static PyObject *new_like(PyObject *t, const View *v) {
   return PyObject_Vectorcall(f_empty_like, args, 1, kw_contiguous);
 }
 
-/* A new tensor of n dimensions (n <= 5) on the device of `on` (on.new_empty(): a fifth less host
- * time than torch.empty() with a device). */
-static PyObject *new_tensor(PyObject *on, int n, const int64_t *shape, PyObject *dtype) {
-  PyObject *size = PyTuple_New(n), *r = NULL;
-  if (!size) return NULL;
-  for (int i = 0; i < n; ++i) {
-    PyObject *x = PyLong_FromLongLong(shape[i]);
-    if (!x) goto done;
-    PyTuple_SET_ITEM(size, i, x);
+static PyObject *tuple_of(int n, const int64_t *x) {
+  PyObject *r = PyTuple_New(n);
+  for (int i = 0; r && i < n; ++i) {
+    PyObject *o = PyLong_FromLongLong(x[i]);
+    if (o)
+      PyTuple_SET_ITEM(r, i, o);
+    else
+      Py_CLEAR(r);
   }
-  PyObject *args[3] = {on, size, dtype};
-  r = PyObject_VectorcallMethod(s_new_empty, args, 2, kw_dtype);
-done:
-  Py_DECREF(size);
+  return r;
+}
+/* A new contiguous tensor of n dimensions (n <= 5) on the device of `on`
+ * (on.new_empty_strided(): half a microsecond less host time than on.new_empty()). */
+static PyObject *new_tensor(PyObject *on, int n, const int64_t *shape, PyObject *dtype) {
+  int64_t stride[5], next = 1;
+  for (int i = n - 1; i >= 0; --i) stride[i] = next, next *= shape[i] > 1 ? shape[i] : 1;
+  PyObject *size = tuple_of(n, shape), *strides = size ? tuple_of(n, stride) : NULL, *r = NULL;
+  if (strides) {
+    PyObject *args[4] = {on, size, strides, dtype};
+    r = PyObject_VectorcallMethod(s_new_empty, args, 3, kw_dtype);
+  }
+  Py_XDECREF(size);
+  Py_XDECREF(strides);
   return r;
 }
 
@@ -562,7 +571,7 @@ static PyMethodDef methods[] = {
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__binding(void) {
-  s_new_empty = PyUnicode_InternFromString("new_empty");
+  s_new_empty = PyUnicode_InternFromString("new_empty_strided");
   if (!s_new_empty) return NULL;
   return PyModule_Create(&module);
 }
