@@ -251,7 +251,7 @@ struct RowMath {
 // small enough for fp32 (below 2^-8, so their roundings below 2^-32), the others are in 64 bits.
 __device__ __forceinline__ void turn_cos_sin(uint64_t t, double &c, double &s) {
   const uint64_t quarter = (t + (1ull << 61)) >> 62;
-  const double y = (double)(int64_t)(t - (quarter << 62)) * 3.4061215800304616e-19;  // 2 pi 2^-64
+  const double y = (double)(int64_t)(t - (quarter << 62)) * 3.4061215800865545e-19;  // 2 pi 2^-64
   const double z = y * y;
   const float w = (float)z;
   const float st = 1.0f / 120 + w * (-1.0f / 5040 + w * (1.0f / 362880 + w * (-1.0f / 39916800)));
