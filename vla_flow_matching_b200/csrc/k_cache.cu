@@ -39,6 +39,11 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
@@ -96,11 +101,15 @@ struct PoolE4m3 {
     const int e = (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u);
     return __uint_as_float((uint32_t)max(e, 1) << 23);
   }
-  static __device__ __forceinline__ uint32_t codes(const float *v, float scale) {
+  template <int N>
+  static __device__ __forceinline__ void codes(const float (&v)[N], float scale, uint32_t (&w)[N / 4]) {
     const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));  // exact: 2^-n of 2^n
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv), __NV_SATFINITE, __NV_E4M3);
-    return lo | hi << 16;
+    uint32_t c[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+      c[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i] * inv, v[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) w[i] = c[2 * i] | c[2 * i + 1] << 16;
   }
   static __device__ __forceinline__ void values(uint32_t w, float *v) {
     const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
@@ -117,17 +126,32 @@ struct PoolInt8 {
   // x / scale, correctly rounded before the last step, so that a code is the nearest one: with
   // the rounded reciprocal r, q = x r and then q + (x - q scale) r is the rounded quotient
   // (Markstein, 1990) as long as the residual is exact, which scales of 2^-100 and more
-  // guarantee.  |x / scale| is at most 127 and a rounding, so the code needs no clamp.
-  static __device__ __forceinline__ uint32_t codes(const float *v, float scale) {
-    const float r = __frcp_rn(scale);
-    int c[4];
+  // guarantee.  |x / scale| is at most 127 and a rounding, so the code needs no clamp, and the sum
+  // with 1.5 * 2^23, where a step is 1, has the rounded integer in its low bits.  (In packed pairs
+  // and without conversions 64 x 816 tokens of one head of 256 dims, written and read back, take
+  // 43.5 us instead of 47.5.)
+  template <int N>
+  static __device__ __forceinline__ void codes(const float (&v)[N], float scale, uint32_t (&w)[N / 4]) {
+    constexpr float kInt = 12582912.0f;
+    float c[N];
+    if (scale >= 7.8886091e-31f) {
+      const float r = __frcp_rn(scale);
+      const f32x2 r2 = pair(r, r), minus = pair(-scale, -scale);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float q = v[i] * r;
-      q = scale >= 7.8886091e-31f ? fmaf(fmaf(-q, scale, v[i]), r, q) : __fdiv_rn(v[i], scale);
-      c[i] = __float2int_rn(q);
+      for (int i = 0; i < N / 2; ++i) {
+        const f32x2 x = pair(v[2 * i], v[2 * i + 1]), q = mul2(x, r2);
+        split(add2(fma2(fma2(q, minus, x), r2, q), pair(kInt, kInt)), c[2 * i], c[2 * i + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) c[i] = __fdiv_rn(v[i], scale) + kInt;
     }
-    return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint32_t lo = __byte_perm(__float_as_uint(c[4 * i]), __float_as_uint(c[4 * i + 1]), 0x0040);
+      const uint32_t hi = __byte_perm(__float_as_uint(c[4 * i + 2]), __float_as_uint(c[4 * i + 3]), 0x0040);
+      w[i] = __byte_perm(lo, hi, 0x5410);
+    }
   }
   static __device__ __forceinline__ void values(uint32_t w, float *v) {
 #pragma unroll
@@ -426,12 +450,10 @@ __global__ void __launch_bounds__(256, kTurned ? 3 : 4) k_rows(const __grid_cons
           const bool finite = top < 0x7f800000u;
           const float scale = finite ? Pool::scale(top) : __uint_as_float(0x7fc00000u);
           uint32_t w[kN / 4] = {}, w2[kN / 4] = {};
-          if (finite)
-#pragma unroll
-            for (int i = 0; i < kN / 4; ++i) {
-              w[i] = Pool::codes(u + 4 * i, scale);
-              w2[i] = Pool::codes(v + 4 * i, scale);
-            }
+          if (finite) {
+            Pool::codes(u, scale, w);
+            Pool::codes(v, scale, w2);
+          }
           uint8_t *dst = (uint8_t *)pool.codes + at * D + l0;
           if constexpr (kN == 8) {
             *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
