@@ -111,11 +111,11 @@ struct PoolE4m3 {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) w[i] = c[2 * i] | c[2 * i + 1] << 16;
   }
-  static __device__ __forceinline__ void values(uint32_t w, float *v) {
+  static __device__ __forceinline__ void values(uint32_t w, f32x2 *v) {
     const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
     const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
     const float2 x = __half22float2(a), y = __half22float2(b);
-    v[0] = x.x, v[1] = x.y, v[2] = y.x, v[3] = y.y;
+    v[0] = pair(x.x, x.y), v[1] = pair(y.x, y.y);
   }
 };
 struct PoolInt8 {
@@ -153,9 +153,13 @@ struct PoolInt8 {
       w[i] = __byte_perm(lo, hi, 0x5410);
     }
   }
-  static __device__ __forceinline__ void values(uint32_t w, float *v) {
+  // x + 128 as the low bits of a float in [2^23, 2^24), whose steps are 1; minus 2^23 + 128.
+  static __device__ __forceinline__ void values(uint32_t w, f32x2 *v) {
+    float x[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = (float)((int)(w << (24 - 8 * i)) >> 24);
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4b000000u, 0x7650 + i));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v[i] = add2(pair(x[2 * i], x[2 * i + 1]), pair(-8388736.0f, -8388736.0f));
   }
 };
 
@@ -542,10 +546,12 @@ __global__ void __launch_bounds__(256) k_cache_read(const __grid_constant__ Read
           } else {
             float x[kN];
             if constexpr (Pool::kScaled) {
+              f32x2 y[kN / 2];
 #pragma unroll
-              for (int j = 0; j < kWords; ++j) Pool::values(w[u][i][c][j], x + 4 * j);
+              for (int j = 0; j < kWords; ++j) Pool::values(w[u][i][c][j], y + 2 * j);
 #pragma unroll
-              for (int j = 0; j < kN; ++j) x[j] *= scale[u][i];
+              for (int j = 0; j < kN / 2; ++j)
+                split(mul2(y[j], pair(scale[u][i], scale[u][i])), x[2 * j], x[2 * j + 1]);
             } else {
 #pragma unroll
               for (int j = 0; j < kWords; ++j) {
