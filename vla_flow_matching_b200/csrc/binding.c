@@ -23,7 +23,13 @@ static PyObject *f_empty_like, *f_device, *f_fail;  /* callables, see setup() */
 static PyObject *kw_contiguous, *v_contiguous, *kw_dtype;
 
 /* Element types by DLPack's code and bits. */
-enum { kBf16 = kDLBfloat << 8 | 16, kF32 = kDLFloat << 8 | 32, kI32 = kDLInt << 8 | 32, kU8 = kDLUInt << 8 | 8, kBool = kDLBool << 8 | 8 };
+enum {
+  kBf16 = kDLBfloat << 8 | 16,
+  kF32 = kDLFloat << 8 | 32,
+  kI32 = kDLInt << 8 | 32,
+  kU8 = kDLUInt << 8 | 8,
+  kBool = kDLBool << 8 | 8
+};
 
 typedef struct {
   char *data;
@@ -207,7 +213,9 @@ static int is_current(long device) {
   return d == -1 && PyErr_Occurred() ? -1 : d == device;
 }
 
-static int current_stream(long device, void **stream) { return api->current_work_stream(kDLCUDA, (int32_t)device, stream); }
+static int current_stream(long device, void **stream) {
+  return api->current_work_stream(kDLCUDA, (int32_t)device, stream);
+}
 
 /* A new contiguous tensor like `t`, whose view is `v`. */
 static PyObject *new_like(PyObject *t, const View *v) {
@@ -551,10 +559,14 @@ static PyObject *py_setup(PyObject *self, PyObject *const *a, Py_ssize_t n) {
   kw_dtype = Py_BuildValue("(s)", "dtype");
   Py_DECREF(low);
   PyObject *capsule = t_tensor ? PyObject_GetAttrString(t_tensor, "__dlpack_c_exchange_api__") : NULL;
-  if (!capsule) return NULL;
+  if (!capsule) {
+    PyErr_SetString(PyExc_ImportError, "this torch does not hand out DLPack's C exchange interface (2.11 does)");
+    return NULL;
+  }
   api = PyCapsule_GetPointer(capsule, "dlpack_exchange_api"); /* lives as long as the process */
   Py_DECREF(capsule);
-  if (api && (api->header.version.major != DLPACK_MAJOR_VERSION || !api->dltensor_from_py_object_no_sync))
+  if (api && (api->header.version.major != DLPACK_MAJOR_VERSION || !api->dltensor_from_py_object_no_sync ||
+              !api->current_work_stream))
     PyErr_SetString(PyExc_ImportError, "this torch has another DLPack exchange interface than the one built against");
   if (PyErr_Occurred()) return NULL;
   Py_RETURN_NONE;
