@@ -226,9 +226,11 @@ int pi0x_cache_read(const pi0x_cache *cache, int layer0, int layers, int B, int 
  * mask_len and mask[b][p] nonzero; nothing else is read.
  *   out (B, q_heads, head_dim) bf16 = softmax(scale * q . k) v; lse (B, q_heads) fp32
  * (may be NULL) = log of the sum of exp(scale * q . k).  A sample without a key gets
- * zeros and -inf.  Sums and softmax statistics are fp32; probabilities are rounded to
- * the 16-bit type of the matrix product.  The result of a call does not depend on
- * timing.
+ * zeros and -inf.  Sums and softmax statistics are fp32.  Probabilities go into the
+ * matrix product as two bf16 values each (exact to 2^-15) beside bf16 pages, as fp16
+ * (2^-11) beside 8-bit ones; there q is fp16 after a division by a power of two, so an
+ * element far below the head's largest is exact to 2^-25 of that one.  The result of a
+ * call does not depend on timing.
  *   workspace: pi0x_cache_attention_workspace() bytes, 16-byte aligned, used by this
  * call only while it runs: calls that may overlap need one each. */
 int pi0x_cache_attention(const pi0x_cache *cache, int layer, int B, int q_heads, const pi0x_rows *q,

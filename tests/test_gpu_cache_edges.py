@@ -1,0 +1,75 @@
+"""Edges of the paged prefix cache on the GPU: how exact what the calls return is, and inputs
+that the contract allows but that are rare.  Tolerances count roundings, as in
+test_gpu_cache.py.
+"""
+import math
+
+import pytest
+import torch
+
+from vla_flow_matching_b200 import build, pi0x
+
+from .test_gpu_cache import BF16, F32, U32, half_step, ints, rng
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _library():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build.build()
+
+
+# ---- attention -----------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("B,H,kv,D,n", [(1, 8, 1, 256, 2), (3, 4, 2, 64, 300), (2, 20, 1, 128, 77), (1, 8, 1, 256, 6000)])
+def test_attention_weights_keep_their_bits(pool, B, H, kv, D, n):
+    """Values of +1 and -1 whose weights are nearly equal: outputs far below the weights, which show
+    what a weight's rounding costs.  Only one element of a query and of a key is not zero, so a
+    score is one product."""
+    g = rng(n + D)
+    ps = 16
+    per = -(-n // ps)
+    c = pi0x.KVCache.empty(1, B * per, ps, kv, D, pool)
+    table = torch.arange(B * per, device="cuda", dtype=torch.int32).view(B, per)
+    code = torch.randint(-7, 8, (B * per, ps, kv), device="cuda", generator=g).float()  # exact in every type
+    c.k[0, ..., 3] = code.to(c.k.dtype)
+    sign = 1.0 - 2.0 * (torch.arange(B * per * ps, device="cuda").view(-1, ps, 1) % 2)
+    c.v[0] = sign[..., None].expand(-1, -1, kv, D).to(c.v.dtype)
+    if pool != "bf16":
+        c.k_scale.fill_(1.0)
+        c.v_scale.fill_(1.0)
+    q = torch.zeros(B, H, D, device="cuda", dtype=BF16)
+    q[..., 3] = 1.0 + torch.arange(H, device="cuda").to(BF16) / 64
+    scale = 0.0013
+    out, lse = c.attend(0, q, table, ints([n] * B), scale=scale)
+    k = code.view(B, per * ps, kv)[:, :n].double()
+    s = torch.einsum("bhg,bnh->bhgn", q[..., 3].double().view(B, kv, -1), k).flatten(1, 2) * scale
+    z = torch.logsumexp(s, -1)
+    p = torch.exp(s - z[..., None])
+    o = (p * sign.view(B, -1)[:, None, :n].double()).sum(-1)
+    # a product and the scale's, the exponential, and the sums of n weights in fp32
+    delta = 8 * U32 * (s.abs().amax(-1) + 1) + n * U32 + 2.0 ** -21
+    weight = 2.0 ** -15 if pool == "bf16" else half_step(torch.float16)
+    tol = half_step(BF16) * o.abs() * (1 + 2 ** -6) + (weight + 2 * delta) * 1.01
+    err = (out.double() - o[..., None]).abs().amax(-1)
+    assert bool((err <= tol).all()), float((err - tol).max())
+    assert bool(((lse.double() - z).abs() <= delta + 4 * U32 * z.abs()).all())
+
+
+@pytest.mark.parametrize("D,H", [(256, 8), (64, 20)])
+@pytest.mark.parametrize("far", [0.0, 30.0])
+def test_infinite_values_stay_infinite(D, H, far):
+    c = pi0x.KVCache.empty(1, 4, 16, 1, D, "bf16")
+    c.v.fill_(1.0)
+    c.v[0, 1, 3, 0, 5], c.v[0, 2, 7, 0, 9] = math.inf, -math.inf
+    c.k[0, 1, 3, 0, 0] = -1.0                                # the infinite value's weight is e^-far
+    q = torch.zeros(1, H, D, device="cuda", dtype=BF16)
+    q[..., 0] = 1.0
+    out, lse = c.attend(0, q, ints([[0, 1, 2, 3]]), ints([64]), scale=far)
+    want = torch.ones_like(out)
+    want[..., 5], want[..., 9] = math.inf, -math.inf
+    assert torch.equal(out, want) and bool(lse.isfinite().all())
