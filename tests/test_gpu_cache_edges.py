@@ -9,7 +9,7 @@ import torch
 
 from vla_flow_matching_b200 import build, pi0x
 
-from .test_gpu_cache import BF16, F32, U32, half_step, ints, rng
+from .test_gpu_cache import BF16, F32, U32, check_attend, half_step, ints, make_cache, randn, rng, scattered
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,23 @@ def test_infinite_values_stay_infinite(D, H, far):
     want = torch.ones_like(out)
     want[..., 5], want[..., 9] = math.inf, -math.inf
     assert torch.equal(out, want) and bool(lse.isfinite().all())
+
+
+@pytest.mark.parametrize("pool", ["e4m3", "int8"])
+@pytest.mark.parametrize("B,H,kv,D,n", [(2, 8, 1, 256, 500), (3, 20, 1, 64, 99), (1, 8, 2, 128, 9000)])
+def test_scales_of_either_sign_and_zero(pool, B, H, kv, D, n):
+    """A row stands for code * scale, whatever the scale's sign."""
+    g = rng(n)
+    per = -(-n // 16)
+    c = make_cache(pool, 1, B * per, 16, kv, D, n)
+    table, lens = scattered(g, B, per, B * per), ints([n - 7 * b for b in range(B)])
+    for s in (c.k_scale, c.v_scale):
+        s.mul_(torch.randint(-1, 2, s.shape, device="cuda", generator=g))
+    q = randn(g, B, H, D, dtype=BF16)
+    out, lse = c.attend(0, q, table, lens)
+    check_attend(c, 0, q, table, lens, None, None, out, lse)
+    c.v_scale.fill_(-0.5)
+    out, lse = c.attend(0, q, table, lens)
+    check_attend(c, 0, q, table, lens, None, None, out, lse)
+    c.v_scale.fill_(0.0)
+    assert not bool(c.attend(0, q, table, lens)[0].any())
