@@ -165,7 +165,8 @@ typedef struct {
 
 /* Rows of `head_dim` contiguous elements at data + b * batch_stride + t * token_stride
  * + h * head_stride (elements); data and the strides are multiples of 16 bytes.
- * An input's rows may share memory (strides of 0), an output's may not. */
+ * An input's rows may share memory (strides of 0), an output's may not: of dimensions
+ * above 1 each stride, from the least on, is beyond all that the lesser ones span. */
 typedef struct {
   void *data;
   int64_t batch_stride, token_stride, head_stride;

@@ -3,6 +3,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <string>
 
 #include "../../include/pi0x.h"
@@ -33,10 +34,23 @@ bool rows_ok(const pi0x_rows *r, int elem) {
   return r && r->data && aligned(r->data) && r->batch_stride % n == 0 && r->token_stride % n == 0 &&
          r->head_stride % n == 0;
 }
-// An output's rows, `head_dim` elements each, do not share memory with the next ones.
+// No two of an output's rows share memory: each stride, from the least on, is beyond all that the
+// lesser ones span.
 bool apart(const pi0x_rows *r, int B, int T, int heads, int head_dim) {
-  auto ok = [&](int n, int64_t stride) { return n < 2 || stride >= head_dim || stride <= -head_dim; };
-  return ok(B, r->batch_stride) && ok(T, r->token_stride) && ok(heads, r->head_stride);
+  typedef __int128 Wide;
+  struct {
+    int n;
+    Wide stride;
+  } dim[3] = {{B, r->batch_stride}, {T, r->token_stride}, {heads, r->head_stride}};
+  for (auto &d : dim) d.stride = d.stride < 0 ? -d.stride : d.stride;
+  std::sort(dim, dim + 3, [](const auto &x, const auto &y) { return x.stride < y.stride; });
+  Wide span = head_dim;
+  for (const auto &d : dim) {
+    if (d.n < 2) continue;
+    if (d.stride < span) return false;
+    span += (d.n - 1) * d.stride;
+  }
+  return true;
 }
 RowsPtr rows_of(const pi0x_rows *r) { return RowsPtr{r->data, r->batch_stride, r->token_stride, r->head_stride}; }
 
