@@ -93,3 +93,26 @@ def test_scales_of_either_sign_and_zero(pool, B, H, kv, D, n):
     check_attend(c, 0, q, table, lens, None, None, out, lse)
     c.v_scale.fill_(0.0)
     assert not bool(c.attend(0, q, table, lens)[0].any())
+
+
+# ---- layouts ---------------------------------------------------------------------------
+
+
+def test_strides_of_dimensions_of_one_do_not_count():
+    """torch leaves the stride of a dimension of size 1 at any value."""
+    g = rng(14)
+    D = 64
+    q = randn(g, 3, 4, D, dtype=BF16)
+    odd = torch.as_strided(q, (3, 1, 4, D), (4 * D, 3, D, 1))
+    start = ints([5, 0, 700])
+    want = pi0x.qk_norm_rope(q[:, None], q[:, None, :1], start)
+    got = pi0x.qk_norm_rope(odd, torch.as_strided(q, (3, 1, 1, D), (4 * D, 1, 7, 1)), start)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    c, d = (pi0x.KVCache.empty(1, 3, 4, 1, D) for _ in range(2))
+    table, slot = ints([[0], [1], [2]]), ints([0, 3, 2])
+    c.write(0, q[:, None, :1], q[:, None, 1:2], table, slot, rope_base=1e4)
+    d.write(0, torch.as_strided(q, (3, 1, 1, D), (4 * D, 1, 7, 1)),
+            torch.as_strided(q, (3, 1, 1, D), (4 * D, 5, 1, 1), D), table, slot, rope_base=1e4)
+    assert torch.equal(c.k, d.k) and torch.equal(c.v, d.v)
+    one = torch.as_strided(q, (1, 4, D), (3, D, 1))
+    assert torch.equal(c.attend(0, one, table[:1], slot[:1] + 1)[0], c.attend(0, q[:1], table[:1], slot[:1] + 1)[0])

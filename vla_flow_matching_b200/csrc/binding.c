@@ -98,6 +98,10 @@ static int has_shape(const View *v, int n, const int64_t *shape) {
   return 1;
 }
 
+/* The stride of dimension i; 0 where its size is 1, since torch leaves such strides at any value
+ * and the library wants whole 16 bytes. */
+static int64_t stride_of(const View *v, int i) { return v->shape[i] > 1 ? v->stride[i] : 0; }
+
 /* A view as (B, T, heads, D) rows of `dtype` with a contiguous last dimension. */
 static int rows_of(const char *what, const char *name, const View *v, int64_t B, int64_t T, int64_t heads, int64_t D,
                    int dtype, pi0x_rows *r) {
@@ -111,9 +115,9 @@ static int rows_of(const char *what, const char *name, const View *v, int64_t B,
     return -1;
   }
   r->data = v->data;
-  r->batch_stride = v->stride[0];
-  r->token_stride = v->stride[1];
-  r->head_stride = v->stride[2];
+  r->batch_stride = stride_of(v, 0);
+  r->token_stride = stride_of(v, 1);
+  r->head_stride = stride_of(v, 2);
   return 0;
 }
 static int take_rows(const char *what, const char *name, PyObject *t, int64_t B, int64_t T, int64_t heads, int64_t D,
@@ -523,7 +527,7 @@ static PyObject *py_cache_attention(PyObject *self, PyObject *const *a, Py_ssize
     const size_t need = pi0x_cache_attention_workspace(c, (int)B, (int)heads, max_pages);
     const int64_t size = (int64_t)need;
     if (need && !(work = out_tensor(what, "workspace", Py_None, NULL, a[3], 1, &size, kU8, &device, &pw))) goto out;
-    const pi0x_rows rq = {q.data, q.stride[0], 0, q.stride[1]};
+    const pi0x_rows rq = {q.data, stride_of(&q, 0), 0, stride_of(&q, 1)};
     void *stream;
     int st;
     if (current_stream(device, &stream)) goto out;
