@@ -2,12 +2,13 @@
 that the contract allows but that are rare.  Tolerances count roundings, as in
 test_gpu_cache.py.
 """
+import dataclasses
 import math
 
 import pytest
 import torch
 
-from vla_flow_matching_b200 import build, pi0x
+from vla_flow_matching_b200 import build, pi0x, synth
 
 from .test_gpu_cache import BF16, F32, U32, check_attend, half_step, ints, make_cache, randn, rng, scattered
 
@@ -116,3 +117,31 @@ def test_strides_of_dimensions_of_one_do_not_count():
     assert torch.equal(c.k, d.k) and torch.equal(c.v, d.v)
     one = torch.as_strided(q, (1, 4, D), (3, D, 1))
     assert torch.equal(c.attend(0, one, table[:1], slot[:1] + 1)[0], c.attend(0, q[:1], table[:1], slot[:1] + 1)[0])
+
+
+# ---- the sampler on a cache ------------------------------------------------------------
+
+
+def test_sampler_buffers_settle_when_shapes_alternate():
+    """After one round of two shapes, neither of which covers the other, calls allocate nothing."""
+    dims = synth.WORKLOADS["tiny"].dims
+    sampler = pi0x.Sampler(dims, synth.make_weights(dims, 0), pi0x.PI0X_BF16)
+    g = rng(15)
+    c = make_cache("bf16", dims.depth, 64, 64, 1, 256, 16)
+    calls, free = [], []
+    for B, P in ((48, 128), (1, 3000)):
+        table = torch.randint(0, 64, (B, -(-P // 64)), device="cuda", generator=g, dtype=torch.int32)
+        calls.append((table, ints([P - b for b in range(B)]), P, randn(g, B, dims.state_dim),
+                      randn(g, B, dims.horizon, dims.action_dim)))
+    first = []
+    for i in range(6):
+        table, lens, P, state, x1 = calls[i % 2]
+        got = sampler.sample_cache(c, table, lens, P, state, x1, 2)
+        sampler.sync()
+        if i < 2:
+            first.append(got)
+        else:
+            assert torch.equal(got, first[i % 2])
+        free.append(torch.cuda.mem_get_info()[0])
+    assert len(set(free[1:])) == 1, free
+    sampler.close()

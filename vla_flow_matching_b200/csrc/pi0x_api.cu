@@ -121,7 +121,6 @@ struct Workspace {
   void *xn, *q, *ks, *vs, *att, *act, *a_emb, *u_emb;
   // host-input staging (device side), allocated lazily
   Arena stage;
-  size_t stage_B = 0, stage_P = 0;
   bf16 *st_k = nullptr, *st_v = nullptr;
   uint8_t *st_mask = nullptr;
   float *st_state = nullptr, *st_x = nullptr;
@@ -413,27 +412,29 @@ int ensure_workspace(pi0x_handle *h, int B, int P, int N) {
   return PI0X_OK;
 }
 
+// Staging buffers for a call of B samples and P slots, cut anew from one allocation, which grows to the
+// largest call's bytes and stays (its layout is not kept in a captured graph: calls pass the pointers).
 int ensure_stage(pi0x_handle *h, int B, int P) {
   Workspace &ws = h->ws;
-  if (ws.stage.base && (size_t)B <= ws.stage_B && (size_t)P <= ws.stage_P) return PI0X_OK;
-  if (h->called) cudaStreamSynchronize(h->last_stream);
-  if (ws.stage.base) cudaFree(ws.stage.base);
-  ws.stage = Arena();
   const int L = h->cfg.depth, H = h->cfg.horizon, A = h->cfg.action_dim, S = h->cfg.state_dim;
-  const size_t kv = (size_t)L * B * (size_t)(P > 0 ? P : 1) * kHeadDim * 2;
-  size_t bytes = 2 * round_up(kv, 1024) + round_up((size_t)B * (P > 0 ? P : 1), 1024) +
-                 round_up(4 * (size_t)B * S, 1024) + round_up(4 * (size_t)B * H * A, 1024) + 8 * 1024;
-  void *base = nullptr;
-  CK(cudaMalloc(&base, bytes));
-  ws.stage.base = (uint8_t *)base;
-  ws.stage.size = bytes;
+  const size_t slots = (size_t)B * (P > 0 ? P : 1), kv = (size_t)L * slots * kHeadDim * 2;
+  const size_t bytes = 2 * round_up(kv, 1024) + round_up(slots, 1024) + round_up(4 * (size_t)B * S, 1024) +
+                       round_up(4 * (size_t)B * H * A, 1024);
+  if (bytes > ws.stage.size) {
+    if (h->called) cudaStreamSynchronize(h->last_stream);
+    if (ws.stage.base) cudaFree(ws.stage.base);
+    ws.stage = Arena();
+    void *base = nullptr;
+    CK(cudaMalloc(&base, bytes));
+    ws.stage.base = (uint8_t *)base;
+    ws.stage.size = bytes;
+  }
+  ws.stage.used = 0;
   ws.st_k = (bf16 *)ws.stage.take(kv);
   ws.st_v = (bf16 *)ws.stage.take(kv);
-  ws.st_mask = (uint8_t *)ws.stage.take((size_t)B * (P > 0 ? P : 1));
+  ws.st_mask = (uint8_t *)ws.stage.take(slots);
   ws.st_state = (float *)ws.stage.take(4 * (size_t)B * S);
   ws.st_x = (float *)ws.stage.take(4 * (size_t)B * H * A);
-  ws.stage_B = B;
-  ws.stage_P = P;
   return PI0X_OK;
 }
 
