@@ -1,5 +1,9 @@
 """What the paged prefix cache's calls take and refuse, seen from the host before any launch (CPU
 only; a call that is taken ends at its launch where there is no device)."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -50,3 +54,50 @@ def test_outputs_that_share_memory_across_dimensions_are_refused(lib, shape, str
 def test_outputs_whose_rows_lie_apart_are_taken(lib, shape, strides):
     assert rope_into(lib, rows(PTR, *strides), shape) != EINVAL
     assert rope_into(lib, rows(PTR, *strides), shape, F32) != EINVAL
+
+
+# ---- the sampler beside another torch, or none ---------------------------------------------
+
+WITHOUT = {
+    "a torch without the exchange interface": "import torch; del torch.Tensor.__dlpack_c_exchange_api__",
+    "no binding": "import sys; sys.modules['vla_flow_matching_b200._binding'] = None",
+    "no torch": "import sys; sys.modules['torch'] = None",
+}
+LOADS = """
+from vla_flow_matching_b200 import pi0x
+assert pi0x.load().pi0x_version() >= 1 and pi0x.Sampler is not None
+try:
+    pi0x.qk_norm_rope(None)
+except ImportError as e:
+    print("refused:", e)
+"""
+
+
+@pytest.mark.parametrize("name", WITHOUT)
+def test_the_library_loads_without_what_only_the_cache_calls_need(lib, name):
+    r = subprocess.run([sys.executable, "-c", WITHOUT[name] + LOADS], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "refused: the paged-cache calls" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("how", ["error", "missing"])
+def test_a_binding_that_does_not_compile_leaves_the_library(monkeypatch, tmp_path, capsys, how):
+    compiled = []
+
+    def run(cmd, **kw):
+        if cmd[0] == "gcc":
+            if how == "missing":
+                raise FileNotFoundError("gcc")
+            return subprocess.CompletedProcess(cmd, 1, "", "no such type")
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        compiled.append(cmd)
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    for name in ("BUILD", "LIB", "BINDING", "NO_BINDING"):
+        monkeypatch.setattr(B, name, str(tmp_path / name), raising=False)
+    open(B.BINDING, "w").close()  # of an earlier build
+    monkeypatch.setattr(B.subprocess, "run", run)
+    assert B.build() == B.LIB and os.path.exists(B.LIB) and not os.path.exists(B.BINDING)
+    assert "paged-cache" in capsys.readouterr().err
+    n = len(compiled)
+    assert B.up_to_date() and B.build() == B.LIB and len(compiled) == n  # not again and again

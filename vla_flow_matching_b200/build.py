@@ -23,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpi0x.so")
 BINDING = os.path.join(PKG, "_binding.so")
+NO_BINDING = os.path.join(BUILD, "binding.failed")  # why the last build made no binding
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -46,7 +47,9 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    made = [LIB] + ([BINDING] if importlib.util.find_spec("torch") else [])
+    made = [LIB]
+    if importlib.util.find_spec("torch"):
+        made.append(NO_BINDING if os.path.exists(NO_BINDING) else BINDING)
     if not all(os.path.exists(p) for p in made):
         return False
     t = min(os.path.getmtime(p) for p in made)
@@ -78,21 +81,38 @@ def build(force: bool = False, verbose: bool = False, extra: list | None = None)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    why = _build_binding(verbose)
+    if os.path.exists(NO_BINDING):
+        os.remove(NO_BINDING)
+    if why:  # the sampler does without, and the paged-cache calls say so
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        with open(NO_BINDING, "w") as f:
+            f.write(why)
+        print(f"_binding.so, which the paged-cache calls need, was not built: {why}", file=sys.stderr)
+    return LIB
+
+
+def _build_binding(verbose: bool) -> str:
+    """Compile csrc/binding.c where there is a torch; returns why it could not be, or ""."""
     torch = importlib.util.find_spec("torch")
     if torch is None:  # the paged-cache calls take torch tensors
-        return LIB
+        return ""
     # finds libpi0x.so beside itself; Python's own symbols are the interpreter's; of torch only the
     # DLPack header is used
     cmd = ["gcc", "-O2", "-Wall", "-Wextra", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
            "-I", os.path.join(torch.submodule_search_locations[0], "include"),
            os.path.join(CSRC, "binding.c"), "-o", BINDING + ".tmp", "-L", PKG, "-l:libpi0x.so", "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        return str(e)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed on binding.c:\n{r.stdout}\n{r.stderr}")
+        return f"gcc failed on binding.c:\n{r.stdout}\n{r.stderr}"
     if verbose and r.stderr:
         print(r.stderr, file=sys.stderr)
     os.replace(BINDING + ".tmp", BINDING)
-    return LIB
+    return ""
 
 
 if __name__ == "__main__":

@@ -98,7 +98,7 @@ def _fail(status: int, what: str):
 
 def load() -> ctypes.CDLL:
     """Load libpi0x.so (built in-tree by vla_flow_matching_b200.build)."""
-    global _lib, _native
+    global _lib
     if _lib is not None:
         return _lib
     if not os.path.exists(_LIB_PATH):
@@ -160,12 +160,27 @@ def load() -> ctypes.CDLL:
     lib.pi0x_cache_attention_workspace.restype = ctypes.c_size_t
     lib.pi0x_sample_cache.argtypes = [ptr, cache, cint, cint, ptr, cint, ptr, ptr, ptr, ptr, cint, ptr, ptr]
     lib.pi0x_sample_cache.restype = cint
-    if torch is not None:
-        from . import _binding
-        _binding.setup(torch, _fail)
-        _native = _binding
     _lib = lib
     return lib
+
+
+def load_binding():
+    """Load libpi0x.so and the paged-cache calls' marshalling (_binding.so), which the first of those
+    calls does by itself.  It needs a torch with DLPack's C exchange interface (2.11 has it);
+    :class:`Sampler` does without."""
+    global _native
+    if _native is None:
+        load()
+        if torch is None:
+            raise ImportError("the paged-cache calls take torch tensors, and torch cannot be imported")
+        try:
+            from . import _binding
+            _binding.setup(torch, _fail)
+        except ImportError as e:
+            raise ImportError(f"the paged-cache calls need _binding.so, built by `python -m "
+                              f"vla_flow_matching_b200.build --force` beside a torch like 2.11: {e}") from e
+        _native = _binding
+    return _native
 
 
 def _ptr(a) -> int:
@@ -227,7 +242,7 @@ def qk_norm_rope(q, k=None, start=None, *, positions=None, q_gain=None, k_gain=N
     Runs on the current stream of the tensors' device.
     """
     if _native is None:
-        load()
+        load_binding()
     r = _native.qk_norm_rope(q, k, start, positions, q_gain, k_gain, eps, rope_base, q_out, k_out)
     if r is NotImplemented:
         with torch.cuda.device(q.device):
@@ -267,7 +282,7 @@ class KVCache:
         self._index = k.device.index
         self._desc = Cache(k.data_ptr(), v.data_ptr(), _ptr(k_scale), _ptr(v_scale), *k.shape, types[k.dtype])
         self._address = ctypes.addressof(self._desc)
-        load()
+        load_binding()
 
     # The descriptor holds these tensors' addresses, so they stay the cache's for its life.
     k = property(lambda self: self._pools[0])
