@@ -175,9 +175,11 @@ typedef struct {
 /* What is done to queries and keys: y = x * rsqrt(mean(x^2) + eps) * (1 + gain) over
  * each head's row where a gain is given, then the rotate-half rotation of the pairs
  * (i, i + head_dim/2) by pos * rope_base^(-2i/head_dim) where rope_base > 0 (1 or
- * more).  The angle is exact to 2^-32 of a turn at every 32-bit position; all of it
- * is fp32 (sines and cosines of bf16 rows that stay bf16 to 2^-20), rounded once to
- * the output's type. */
+ * more).  At every 32-bit position the angle is exact to 1.5 * 2^-32 of a turn for
+ * bases of 100 and more (4.3 * 2^-32 for all); the rest is fp32 (sines and cosines of
+ * bf16 rows that stay bf16 to 2^-20; 64 bits for keys on their way into e4m3 pages),
+ * rounded once to the output's type.  Squares are summed in fp32: a row of values of
+ * 2^60 and more may leave its norm as zeros. */
 typedef struct {
   const float *q_gain, *k_gain;  /* (head_dim) fp32; NULL: no norm */
   const int32_t *positions;      /* (B, T); NULL: start[b] + t */

@@ -10,7 +10,7 @@ import torch
 
 from vla_flow_matching_b200 import build, pi0x, synth
 
-from .test_gpu_cache import BF16, F32, U32, check_attend, half_step, ints, make_cache, randn, rng, scattered
+from .test_gpu_cache import BF16, F32, U32, check_attend, half_step, ints, make_cache, randn, rng, rotated, scattered
 
 pytestmark = pytest.mark.gpu
 
@@ -94,6 +94,49 @@ def test_scales_of_either_sign_and_zero(pool, B, H, kv, D, n):
     check_attend(c, 0, q, table, lens, None, None, out, lse)
     c.v_scale.fill_(0.0)
     assert not bool(c.attend(0, q, table, lens)[0].any())
+
+
+# ---- codes -------------------------------------------------------------------------------
+
+
+def e4m3_of(y):
+    """Values that rows of y (64 bits) stand for in e4m3 pages, and their scales, in 64 bits throughout."""
+    part, power = torch.frexp(y.abs().amax(-1) / 448)  # exact at 448 * 2^n
+    scale = torch.ldexp(torch.ones_like(part), torch.clamp(power - (part == 0.5).int(), min=-126))
+    scale = torch.where(y.abs().amax(-1) == 0, 2.0 ** -126, scale)
+    x = y / scale[..., None]
+    step = torch.ldexp(torch.ones_like(x), torch.frexp(x.abs().clamp_min(2.0 ** -6))[1] - 4)
+    return (x / step).round() * step, scale
+
+
+@pytest.mark.parametrize("D,dtype,size,rounds,most", [
+    (256, BF16, 1.0, 32, 6),              # 67 million values
+    (128, F32, 1.0, 2, 2), (64, F32, 1.0, 2, 2),
+    (256, F32, 2.0 ** -136, 1, 2), (64, BF16, 2.0 ** -131, 1, 2)])  # codes below 2^-126, where fp32 holds fewer bits
+def test_e4m3_codes_are_those_of_the_formula(D, dtype, size, rounds, most):
+    """Keys normed and rotated on their way into e4m3 pages have the 64-bit formula's codes.  Sines and
+    cosines are exact to 2^-32, so a code may differ where a value lies that near to the border of two:
+    about 2^-31 * 11 borders a value * 4 (pairs longer than their halves), 1 in 50 million.  In fp32 it
+    is 1 in 2.5 million."""
+    g = rng(D)
+    B, T = 16, 2 ** 17 // D
+    ps = 64
+    c = pi0x.KVCache.empty(1, B * T // ps, ps, 1, D, "e4m3")
+    table = torch.arange(B * T // ps, device="cuda", dtype=torch.int32).view(B, -1)
+    zero = ints([0] * B)
+    wrong = 0
+    for i in range(rounds):
+        k = (randn(g, B, T, 1, D) * size).to(dtype)
+        gain, first = 0.2 * randn(g, D), torch.randint(0, 3000, (B, T), device="cuda", generator=g, dtype=torch.int32)
+        c.write(0, k, k, table, zero, positions=first, k_gain=gain, rope_base=1e4)
+        y = rotated(k, gain, first, 1e4, eps=float(torch.tensor(1e-6)))
+        want, scale = e4m3_of(y)
+        assert torch.equal(c.k_scale.view(B, T, 1).double(), scale)
+        wrong += int((c.k.float().view(B, T, 1, D).double() != want).sum())
+        want, scale = e4m3_of(k.double())  # values as they are: every code
+        assert torch.equal(c.v_scale.view(B, T, 1).double(), scale)
+        assert torch.equal(c.v.float().view(B, T, 1, D).double(), want)
+    assert wrong <= most, wrong
 
 
 # ---- layouts ---------------------------------------------------------------------------
