@@ -188,3 +188,24 @@ def test_sampler_buffers_settle_when_shapes_alternate():
         free.append(torch.cuda.mem_get_info()[0])
     assert len(set(free[1:])) == 1, free
     sampler.close()
+
+
+def test_sampler_on_a_cache_refuses_wrong_states_and_noise():
+    dims = synth.WORKLOADS["tiny"].dims
+    sampler = pi0x.Sampler(dims, synth.make_weights(dims, 0), pi0x.PI0X_BF16)
+    c = pi0x.KVCache.empty(dims.depth, 4, 16)
+    table, lens = ints([[0], [1]]), ints([16, 3])
+    state, x1 = (torch.zeros(2, *shape, device="cuda") for shape in ((dims.state_dim,), (dims.horizon, dims.action_dim)))
+    for bad in (dict(state=state[:1]), dict(x1=x1[:1]), dict(state=state.double()), dict(x1=x1.to(BF16)),
+                dict(x1=x1.transpose(1, 2)), dict(state=state[:, ::2]), dict(x0=x1[:1]), dict(x0=x1.double()),
+                dict(state=state.cpu().numpy()[:1]), dict(state=None), dict(x1=[0.0])):
+        kw = dict(state=state, x1=x1)
+        kw.update(bad)
+        with pytest.raises((ValueError, pi0x.Pi0xError)):
+            sampler.sample_cache(c, table, lens, 16, num_steps=1, **kw)
+    got = sampler.sample_cache(c, table, lens, 16, state, x1, 1)
+    sampler.sync()
+    host = sampler.sample_cache(c, table, lens, 16, state.cpu().numpy(), x1.cpu().numpy(), 1)
+    sampler.sync()
+    assert torch.equal(got.cpu(), torch.from_numpy(host))
+    sampler.close()

@@ -348,6 +348,14 @@ class KVCache:
                           self.head_dim ** -0.5 if scale is None else scale, out, lse)
 
 
+def _is_floats(a, n: int, device) -> bool:
+    """Whether `a` is n contiguous float32 values, a numpy array or a tensor on the host or `device`."""
+    if isinstance(a, np.ndarray):
+        return a.dtype == np.float32 and a.size == n and a.flags.c_contiguous
+    return isinstance(a, torch.Tensor) and a.dtype == torch.float32 and a.numel() == n and a.is_contiguous() and \
+        (a.device.type == "cpu" or a.device == device)
+
+
 class Sampler:
     """A pi0x handle: expert weights on the device plus the loop's workspace.
 
@@ -429,6 +437,12 @@ class Sampler:
                                   not t.is_contiguous()):
                 raise ValueError(f"Sampler.sample_cache: {name} must be a contiguous {dtypes[0]} tensor of shape "
                                  f"{tuple(shape)} on {cache.device}")
+        d = self.dims
+        for name, a, n in (("state", state, B * d.state_dim), ("x1", x1, B * d.horizon * d.action_dim),
+                           ("x0", x0, B * d.horizon * d.action_dim)):
+            if (a is not None or name != "x0") and not _is_floats(a, n, cache.device):
+                raise ValueError(f"Sampler.sample_cache: {name} must be {n} contiguous float32 values for a batch of "
+                                 f"{B}, on the host or {cache.device}")
         if x0 is None:
             x0 = x1.new_empty(x1.shape) if hasattr(x1, "new_empty") else np.empty_like(x1)
         with torch.cuda.device(cache.device):
