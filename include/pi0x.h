@@ -153,7 +153,7 @@ int pi0x_sync_status(pi0x_handle *h);
 
 /* Pages of `page_size` rows for each of `layers` layers.  A row is one position's
  * (kv_heads, head_dim) keys or values; in the 8-bit types every (row, head) has an
- * fp32 scale and stands for code * scale.  kv_heads >= 1; head_dim 64, 128 or 256;
+ * fp32 scale and stands for code * scale.  1 <= kv_heads <= 65535; head_dim 64, 128 or 256;
  * layers >= 1; layers * num_pages * page_size < 2^31; a page table has fewer than 2^31 -
  * 4096 slots. */
 typedef struct {
@@ -224,7 +224,8 @@ int pi0x_cache_read(const pi0x_cache *cache, int layer0, int layers, int B, int 
 
 /* Attention of one new token a sample over the pages of `layer`: q (B, q_heads,
  * head_dim) bf16 (q->token_stride is not used), query head h reads kv head
- * h / (q_heads / kv_heads); q_heads is a multiple of kv_heads.  Keys are the slots p <
+ * h / (q_heads / kv_heads); q_heads is a multiple of kv_heads, and B and q_heads are at most
+ * 65535, B * q_heads and all tables' slots / 64 below 2^31.  Keys are the slots p <
  * lens[b] whose page is inside the pool and, with mask (B, mask_len) uint8, p <
  * mask_len and mask[b][p] nonzero; nothing else is read.
  *   out (B, q_heads, head_dim) bf16 = softmax(scale * q . k) v; lse (B, q_heads) fp32

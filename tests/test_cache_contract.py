@@ -56,6 +56,36 @@ def test_outputs_whose_rows_lie_apart_are_taken(lib, shape, strides):
     assert rope_into(lib, rows(PTR, *strides), shape, F32) != EINVAL
 
 
+# ---- attention's workspace and sizes -------------------------------------------------------
+
+EVEN = [dict(), dict(dtype=E4M3, k_scale=PTR, v_scale=PTR), dict(dtype=INT8, k_scale=PTR, v_scale=PTR, head_dim=256)]
+
+
+@no_gpu
+@pytest.mark.parametrize("kw", EVEN, ids=str)
+@pytest.mark.parametrize("heads", [8, 40])
+def test_attention_refuses_a_missing_or_short_workspace(lib, kw, heads):
+    """A table of 65536 slots is shared out evenly, with parts in the workspace."""
+    c, pages = cache(**kw), 4096
+    need = lib.pi0x_cache_attention_workspace(c, 1, heads, pages)
+    assert need > 0
+
+    def call(work, size):
+        return lib.pi0x_cache_attention(c, 0, 1, heads, rows(), PTR, pages, PTR, None, 0, 1.0, PTR, None, work, size, None)
+
+    for work, size in ((None, need), (PTR + 4, need), (PTR, need - 1), (PTR, 0)):
+        assert call(work, size) == EINVAL and b"workspace" in lib.pi0x_last_error()
+    assert call(PTR, need) != EINVAL
+
+
+@pytest.mark.parametrize("B,heads,pages", [(65536, 8, 4096), (1, 131072, 4096), (60000, 60000, 64), (65535, 8, 1 << 23)])
+def test_sizes_that_attention_refuses_need_no_workspace(lib, B, heads, pages):
+    c = cache()
+    assert lib.pi0x_cache_attention(c, 0, B, heads, rows(), PTR, pages, PTR, None, 0, 1.0, PTR, None, PTR, 1 << 50,
+                                    None) == EINVAL
+    assert lib.pi0x_cache_attention_workspace(c, B, heads, pages) == 0
+
+
 # ---- the sampler beside another torch, or none ---------------------------------------------
 
 WITHOUT = {

@@ -87,6 +87,17 @@ void set_rotation(RowArgs &a, const pi0x_rotation *rot, int head_dim) {
   if (a.rotate) set_ratios(a, rot->rope_base, head_dim);
 }
 
+// The sizes of an attention call on a cache that check_cache() has seen.
+int check_attend(const pi0x_cache *c, int B, int q_heads, int max_pages) {
+  if (q_heads < 1 || q_heads % c->kv_heads)
+    return refuse(PI0X_EINVAL, "pi0x_cache_attention: no heads, or heads that kv_heads does not divide");
+  if (B > 65535 || q_heads > 65535 || (int64_t)B * q_heads > INT32_MAX)
+    return refuse(PI0X_EINVAL, "pi0x_cache_attention: over 65535 samples or heads, or 2^31 rows or more");
+  if ((int64_t)B > INT32_MAX / (((int64_t)max_pages * c->page_size + 63) / 64))
+    return refuse(PI0X_EINVAL, "pi0x_cache_attention: 2^31 blocks of 64 slots or more");
+  return PI0X_OK;
+}
+
 }  // namespace
 
 int check_cache(const pi0x_cache *c, int layer0, int layers, int B, const int32_t *table, int max_pages) {
@@ -218,7 +229,7 @@ int pi0x_cache_read(const pi0x_cache *cache, int layer0, int layers, int B, int 
 
 size_t pi0x_cache_attention_workspace(const pi0x_cache *c, int B, int q_heads, int max_pages) {
   int dummy = 0;
-  if (check_cache(c, 0, 1, B, &dummy, max_pages) || q_heads < 1 || q_heads % c->kv_heads) return 0;
+  if (check_cache(c, 0, 1, B, &dummy, max_pages) || check_attend(c, B, q_heads, max_pages)) return 0;
   return attend_workspace(B, q_heads, c->kv_heads, c->head_dim, c->dtype, c->page_size, max_pages);
 }
 
@@ -227,15 +238,12 @@ int pi0x_cache_attention(const pi0x_cache *cache, int layer, int B, int q_heads,
                          float scale, void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
   const int st = check_cache(cache, layer, 1, B, table, max_pages);
   if (st) return st;
-  if (q_heads < 1 || q_heads % cache->kv_heads || !lens || !aligned(lens, 4) || !out || !aligned(out) ||
-      !aligned(lse, 4) || !rows_ok(q, 2) || (mask && mask_len < 1) || !isfinite(scale * kLog2e))
-    return refuse(PI0X_EINVAL,
-                  "pi0x_cache_attention: heads that kv_heads does not divide, a null or misaligned pointer, an empty "
-                  "mask or a scale that is not finite or beyond 2e38");
-  if (B > 65535 || q_heads > 65535 || (int64_t)B * q_heads > INT32_MAX)
-    return refuse(PI0X_EINVAL, "pi0x_cache_attention: over 65535 samples or heads, or 2^31 rows or more");
-  if ((int64_t)B > INT32_MAX / (((int64_t)max_pages * cache->page_size + 63) / 64))
-    return refuse(PI0X_EINVAL, "pi0x_cache_attention: 2^31 blocks of 64 slots or more");
+  const int sizes = check_attend(cache, B, q_heads, max_pages);
+  if (sizes) return sizes;
+  if (!lens || !aligned(lens, 4) || !out || !aligned(out) || !aligned(lse, 4) || !rows_ok(q, 2) ||
+      (mask && mask_len < 1) || !isfinite(scale * kLog2e))
+    return refuse(PI0X_EINVAL, "pi0x_cache_attention: a null or misaligned pointer, an empty mask or a scale that is "
+                               "not finite or beyond 2e38");
   const size_t need =
       attend_workspace(B, q_heads, cache->kv_heads, cache->head_dim, cache->dtype, cache->page_size, max_pages);
   if (need && (!workspace || !aligned(workspace) || workspace_bytes < need))
