@@ -86,6 +86,15 @@ def test_sizes_that_attention_refuses_need_no_workspace(lib, B, heads, pages):
     assert lib.pi0x_cache_attention_workspace(c, B, heads, pages) == 0
 
 
+@no_gpu
+@pytest.mark.parametrize("t", [3, -5, 2 ** 62 + 1])
+def test_attention_does_not_use_the_token_stride(lib, t):
+    call = [cache(), 0, 1, 8, rows(t=t), PTR, 4, PTR, None, 0, 1.0, PTR, None, None, 0, None]
+    assert lib.pi0x_cache_attention(*call) != EINVAL
+    call[4] = rows(t=t, h=100)
+    assert lib.pi0x_cache_attention(*call) == EINVAL
+
+
 # ---- the sampler beside another torch, or none ---------------------------------------------
 
 WITHOUT = {

@@ -240,7 +240,8 @@ int pi0x_cache_attention(const pi0x_cache *cache, int layer, int B, int q_heads,
   if (st) return st;
   const int sizes = check_attend(cache, B, q_heads, max_pages);
   if (sizes) return sizes;
-  if (!lens || !aligned(lens, 4) || !out || !aligned(out) || !aligned(lse, 4) || !rows_ok(q, 2) ||
+  const pi0x_rows one = q ? pi0x_rows{q->data, q->batch_stride, 0, q->head_stride} : pi0x_rows{};  // a token a sample
+  if (!lens || !aligned(lens, 4) || !out || !aligned(out) || !aligned(lse, 4) || !rows_ok(&one, 2) ||
       (mask && mask_len < 1) || !isfinite(scale * kLog2e))
     return refuse(PI0X_EINVAL, "pi0x_cache_attention: a null or misaligned pointer, an empty mask or a scale that is "
                                "not finite or beyond 2e38");
