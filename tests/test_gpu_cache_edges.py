@@ -162,6 +162,18 @@ def test_strides_of_dimensions_of_one_do_not_count():
     assert torch.equal(c.attend(0, one, table[:1], slot[:1] + 1)[0], c.attend(0, q[:1], table[:1], slot[:1] + 1)[0])
 
 
+def test_reads_of_no_slots_take_their_mask():
+    c = pi0x.KVCache.empty(2, 3, 4, 1, 64)
+    table, lens = ints([[0, 1], [2, -1]]), ints([5, 0])
+    for mask in (None, torch.zeros(2, 0, dtype=torch.uint8, device="cuda"), torch.zeros(2, 0, dtype=bool, device="cuda")):
+        k, v, seen = c.read(table, lens, 0, mask=mask)
+        assert k.shape == v.shape == (2, 2, 1, 0, 64) and seen.shape == (2, 0) and seen.dtype == torch.uint8
+    with pytest.raises(ValueError):
+        c.read(table, lens, 3, mask=torch.zeros(2, 0, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        c.read(table, lens, 0, mask=torch.zeros(2, 1, dtype=torch.uint8, device="cuda"))
+
+
 # ---- the sampler on a cache ------------------------------------------------------------
 
 

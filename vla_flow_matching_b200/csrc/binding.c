@@ -173,8 +173,8 @@ static int take_table(const char *what, PyObject *t, int64_t *B, const int32_t *
   return 0;
 }
 
-/* (B, length) uint8 or bool mask, or None (NULL, 0). */
-static int take_mask(const char *what, PyObject *t, int64_t B, const uint8_t **p, int64_t *length, int *dtype,
+/* (B, length) uint8 or bool mask, length `least` or more, or None (NULL, 0). */
+static int take_mask(const char *what, PyObject *t, int64_t B, int least, const uint8_t **p, int64_t *length, int *dtype,
                      long *device) {
   View v;
   *p = NULL;
@@ -182,10 +182,10 @@ static int take_mask(const char *what, PyObject *t, int64_t B, const uint8_t **p
   *dtype = 0;
   if (t == Py_None) return 0;
   if (take(what, t, &v, device)) return -1;
-  if ((v.dtype != kU8 && v.dtype != kBool) || v.ndim != 2 || v.shape[0] != B || v.shape[1] < 1 ||
+  if ((v.dtype != kU8 && v.dtype != kBool) || v.ndim != 2 || v.shape[0] != B || v.shape[1] < least ||
       v.shape[1] > INT32_MAX || !contiguous(&v)) {
-    PyErr_Format(PyExc_ValueError, "%s: mask must be a contiguous uint8 or bool tensor of shape (%lld, 1 or more)", what,
-                 (long long)B);
+    PyErr_Format(PyExc_ValueError, "%s: mask must be a contiguous uint8 or bool tensor of shape (%lld, %d or more)", what,
+                 (long long)B, least);
     return -1;
   }
   *p = (const uint8_t *)v.data;
@@ -446,9 +446,9 @@ static PyObject *py_cache_read(PyObject *self, PyObject *const *a, Py_ssize_t n)
     return NULL;
   }
   if (take_table(what, a[2], &B, &table, &max_pages, &device) || fits(what, B, 0, 0) ||
-      take_ints(what, "lens", a[3], 1, &B, &lens, &device) || take_mask(what, a[5], B, &mask, &mask_len, &mask_type, &device))
+      take_ints(what, "lens", a[3], 1, &B, &lens, &device) || take_mask(what, a[5], B, 0, &mask, &mask_len, &mask_type, &device))
     return NULL;
-  if (a[3] == Py_None || (mask && mask_len != length)) {
+  if (a[3] == Py_None || (a[5] != Py_None && mask_len != length)) {
     PyErr_Format(PyExc_ValueError, "%s: lens is required, and a mask covers the %d slots read", what, length);
     return NULL;
   }
@@ -504,7 +504,7 @@ static PyObject *py_cache_attention(PyObject *self, PyObject *const *a, Py_ssize
   int64_t B = q.shape[0];
   const int64_t heads = q.shape[1];
   if (fits(what, B, heads, 0) || take_table(what, a[4], &B, &table, &max_pages, &device) ||
-      take_ints(what, "lens", a[5], 1, &B, &lens, &device) || take_mask(what, a[6], B, &mask, &mask_len, &mask_type, &device))
+      take_ints(what, "lens", a[5], 1, &B, &lens, &device) || take_mask(what, a[6], B, 1, &mask, &mask_len, &mask_type, &device))
     return NULL;
   if (a[5] == Py_None) {
     PyErr_Format(PyExc_ValueError, "%s: lens is required", what);
