@@ -10,7 +10,8 @@ import torch
 
 from vla_flow_matching_b200 import build, pi0x, synth
 
-from .test_gpu_cache import BF16, F32, U32, check_attend, half_step, ints, make_cache, randn, rng, rotated, scattered
+from .test_gpu_cache import (BF16, F32, U32, check_attend, check_rotated, half_step, ints, make_cache, randn, rng, rotated,
+                             rotated_slack, scattered, slots)
 
 pytestmark = pytest.mark.gpu
 
@@ -139,6 +140,39 @@ def test_e4m3_codes_are_those_of_the_formula(D, dtype, size, rounds, most):
     assert wrong <= most, wrong
 
 
+@pytest.mark.parametrize("pool", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D,hq,kv,norm,base", [
+    (64, 6, 2, True, 1e4), (128, 3, 1, False, 1e2), (256, 8, 1, True, 5e5), (256, 0, 3, True, None), (64, 1, 1, False, 1.0)])
+def test_rows_are_turned_at_their_positions_on_the_way_in(pool, dtype, D, hq, kv, norm, base):
+    """Positions other than the slots; rows of both types and every head dim into pages of every type."""
+    g = rng(D + kv)
+    B, T, ps = 3, 23, 8
+    c = pi0x.KVCache.empty(1, 3 * 6, ps, kv, D, pool)
+    table, start, count = scattered(g, B, 6, c.num_pages), ints([0, 17, 4]), ints([23, 9, 0])
+    pos = torch.randint(-1000, 200000, (B, T), device="cuda", generator=g, dtype=torch.int32)
+    q = randn(g, B, T, hq, D, dtype=dtype) if hq else None
+    k, v = randn(g, B, T, kv, D, dtype=dtype), randn(g, B, T, kv, D, dtype=dtype)
+    gq, gk = (0.2 * randn(g, D) if norm else None for _ in range(2))
+    qo = c.write(0, k, v, table, start, count, q=q, positions=pos, q_gain=gq if hq else None, k_gain=gk, rope_base=base)
+    if hq:
+        check_rotated(qo, q, gq, pos, base)
+    y = rotated(k, gk, pos, base)
+    for b in range(B):
+        first, n = int(start[b]), int(count[b])
+        for name, want in (("k", y[b, :n]), ("v", v[b, :n].double())):
+            got, _ = slots(c, 0, name, table, b, first + n)
+            top = want.abs().amax(-1, keepdim=True)
+            # half a step: of the value (bf16, e4m3) or of the scale (int8); e4m3's least step is 2^-9 of
+            # a scale that is at most top / 224
+            step = {"bf16": half_step(BF16) * want.abs(), "int8": top / 254 * (1 + 2 ** -10),
+                    "e4m3": 2.0 ** -4 * want.abs() + top / 224 * 2.0 ** -10}[pool]
+            slack = 2 * rotated_slack(want) if name == "k" else 0.0
+            assert bool(((got[first:] - want).abs() <= step * (1 + 2 ** -7) + slack).all()), (b, name)
+        before, _ = slots(c, 0, "k", table, b, first)
+        assert not bool(before.any())
+
+
 # ---- layouts ---------------------------------------------------------------------------
 
 
@@ -220,4 +254,23 @@ def test_sampler_on_a_cache_refuses_wrong_states_and_noise():
     host = sampler.sample_cache(c, table, lens, 16, state.cpu().numpy(), x1.cpu().numpy(), 1)
     sampler.sync()
     assert torch.equal(got.cpu(), torch.from_numpy(host))
+    sampler.close()
+
+
+@pytest.mark.parametrize("pool", ["bf16", "e4m3"])
+def test_fp32_sampler_on_a_cache_matches_contiguous_prefixes(pool):
+    dims = synth.WORKLOADS["tiny"].dims
+    sampler = pi0x.Sampler(dims, synth.make_weights(dims, 0), pi0x.PI0X_FP32)
+    g = rng(17)
+    B, P = 2, 70
+    c = make_cache(pool, dims.depth, 12, 16, 1, 256, 18)
+    table, lens = scattered(g, B, 5, 12), ints([70, 31])
+    mask = (torch.rand(B, P, device="cuda", generator=g) < 0.9).to(torch.uint8)
+    state, x1 = randn(g, B, dims.state_dim), randn(g, B, dims.horizon, dims.action_dim)
+    k, v, seen = c.read(table, lens, P, mask=mask)
+    want = sampler.sample([x.contiguous() for x in k[:, :, 0]], [x.contiguous() for x in v[:, :, 0]], seen, state, x1, 2)
+    sampler.sync()
+    got = sampler.sample_cache(c, table, lens, P, state, x1, 2, mask=mask)
+    sampler.sync()
+    assert torch.equal(got, want) and bool(got.isfinite().all())
     sampler.close()
