@@ -196,6 +196,20 @@ def test_strides_of_dimensions_of_one_do_not_count():
     assert torch.equal(c.attend(0, one, table[:1], slot[:1] + 1)[0], c.attend(0, q[:1], table[:1], slot[:1] + 1)[0])
 
 
+def test_inputs_that_require_gradients_are_plain_data():
+    g = rng(19)
+    q, k = (torch.nn.Parameter(randn(g, 2, 3, h, 64, dtype=BF16)) for h in (4, 2))
+    gain = torch.nn.Parameter(0.1 * randn(g, 64))
+    c, d = (pi0x.KVCache.empty(1, 2, 4, 2, 64) for _ in range(2))
+    table, zero = ints([[0], [1]]), ints([0, 0])
+    got = c.write(0, k, k * 2, table, zero, q=q, q_gain=gain, rope_base=1e4)
+    want = d.write(0, k.detach(), k.detach() * 2, table, zero, q=q.detach(), q_gain=gain.detach(), rope_base=1e4)
+    assert torch.equal(got, want) and torch.equal(c.k, d.k) and torch.equal(c.v, d.v)
+    out, lse = c.attend(0, q[:, 0], table, zero + 3)
+    assert not (got.requires_grad or out.requires_grad or lse.requires_grad)
+    assert torch.equal(out, d.attend(0, q[:, 0].detach(), table, zero + 3)[0])
+
+
 def test_reads_of_no_slots_take_their_mask():
     c = pi0x.KVCache.empty(2, 3, 4, 1, 64)
     table, lens = ints([[0, 1], [2, -1]]), ints([5, 0])

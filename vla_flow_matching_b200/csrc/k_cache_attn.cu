@@ -8,7 +8,8 @@
 // far below the tensor cores' share, above what the FP32 pipes could do beside the loads.
 // So the products go to the tensor cores with the small side, the heads, as the 8
 // columns of m16n8k16: S^T = K Q^T takes 16 keys as rows, O^T = V^T P^T 16 dims, and the
-// scores' layout transposed 8 x 8 is the weights' layout.
+// scores' layout transposed 8 x 8 is the weights' layout.  Beside bf16 pages a weight is two
+// bf16 values, and its product two.
 //
 // A warp works through steps of 16 to 64 keys on its own: it copies their rows, whole rows at
 // a time, into a ring of three buffers (K, V, K, ...) in shared memory and reads operands
@@ -872,9 +873,9 @@ namespace {
 // and values in every CTA.  Clusters where that is the larger cost, and only while the even
 // share is small: with more work the second kernel hardly shows, and ragged samples keep the CTAs
 // of a cluster waiting (lengths are not known here: the page tables' are taken).  GPU time of a
-// call in us, clusters / even shares: 1 x 816 bf16 keys of 256 dims 7.1 / 8.5, 1 x 4096
-// 13.9 / 8.6, 40 x 1000-2000 17.8 / 19.7, 128 x 600-816 21.1 / 23.9, 256 x 600-816 35.4 /
-// 41.0; 512 x 300-700 int8 keys of 64 dims 13.9 / 23.7.
+// call in us, clusters / even shares: 1 x 816 bf16 keys of 256 dims 7.2 / 8.6, 1 x 4096
+// 14.0 / 8.7, 40 x 1000-2000 18.6 / 20.2, 128 x 600-816 21.7 / 24.1, 256 x 600-816 35.9 /
+// 40.8; 512 x 300-700 int8 keys of 64 dims 14.2 / 24.1.
 struct Plan {
   int cluster;  // CTAs of a cluster, 0: even shares and a join
   int grid;
@@ -937,8 +938,8 @@ cudaError_t attend_go(const AttendArgs &a, cudaStream_t s) {
   const int64_t units = (int64_t)a.B * a.kv * head_groups(a.heads, a.kv, S::kHeads);
   const int lists = (int)(units < p.grid ? units : p.grid);
   // Shares of a split unit: about one CTA an SM in all, of 16 vectors or more, of 4 where a unit
-  // has 128 parts or more (1 x 4096 keys in 64 parts: 8.8 us with 16 vectors, 10.0 with 4;
-  // 1 x 32768 in 256: 14.7 and 14.1).
+  // has 128 parts or more (1 x 4096 keys in 64 parts: 8.7 us with 16 vectors, 10.0 with 4;
+  // 1 x 32768 in 256: 14.8 and 14.0).
   const int finest = p.grid / lists >= 128 ? D / 2 : D / 8;
   int shares = 2 * NT * D / kJoinThreads > 1 ? 2 * NT * D / kJoinThreads : 1;
   while (shares < finest && lists * shares * 2 <= 148) shares *= 2;

@@ -239,7 +239,9 @@ def qk_norm_rope(q, k=None, start=None, *, positions=None, q_gain=None, k_gain=N
     dimension.  Token t of sample b has position ``positions[b, t]``, or
     ``start[b] + t`` (start None: 0).  ``rope_base`` None: no rotation.  Returns
     (q_out, k_out), new tensors unless given; an output may be its own input.
-    Runs on the current stream of the tensors' device.
+    Runs on the current stream of the tensors' device.  For inference: no gradient
+    flows back, also where an input requires one, and autograd does not see what is
+    written in place.
     """
     if _native is None:
         load_binding()
@@ -259,6 +261,8 @@ class KVCache:
     Which pages a sample has is the caller's: every method takes ``table`` (B,
     max_pages) int32 page numbers; an entry outside the pool holds no keys.  Methods
     run on the current stream of the cache's device, and may be captured into a graph.
+    For inference: no method has a backward pass, inputs that require gradients are
+    taken as plain data, and autograd does not see writes to pools and given outputs.
     """
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
